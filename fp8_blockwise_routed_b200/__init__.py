@@ -129,6 +129,19 @@ def lib() -> ctypes.CDLL:
         L.moe_ffn_mx_intermediate.restype = i32
         L.moe_ffn_mx_intermediate.argtypes = [P, i64, i32, i32, i32, ctypes.POINTER(ctypes.c_void_p),
                                               ctypes.POINTER(ctypes.c_void_p)]
+        L.moe_balance_loss_workspace_bytes.restype = sz
+        L.moe_balance_loss_workspace_bytes.argtypes = [i64, i32]
+        L.moe_balance_loss.restype = i32
+        L.moe_balance_loss.argtypes = [P, i64, i32, P, P, P, P, P, sz, P]
+        L.moe_route_backward.restype = i32
+        L.moe_route_backward.argtypes = [P, i64, i32, P, P, i32, P, P, i32, ctypes.c_float, P, P, P, P]
+        L.moe_lora.restype = i32
+        L.moe_lora.argtypes = [P, i64, i64, i32, P, P, P, i32, i32, i32, P, P, P, i64, P, P, i64, P, P]
+        L.moe_lora_backward_workspace_bytes.restype = sz
+        L.moe_lora_backward_workspace_bytes.argtypes = [i64, i32]
+        L.moe_lora_backward.restype = i32
+        L.moe_lora_backward.argtypes = [P, i64, i64, i32, P, P, P, i32, i32, i32, P, P, P, P, i64, P, i64, P, i64,
+                                        P, P, P, sz, P]
         L.moe_debug_grouped_down_mx.restype = i32
         L.moe_debug_grouped_down_mx.argtypes = [P, P, i64, i32, i32, P, P, P, i32, i32, P, P, P, P, sz, P]
         _lib = L
@@ -153,6 +166,50 @@ def _check(code: int, what: str):
     if code != 0:
         detail = lib().moe_last_error().decode() if code in (2, 5) else ""
         raise MoeError(code, what, detail)
+
+
+def _refuse(what: str, detail: str):
+    raise MoeError(1, what, detail)
+
+
+def _arg(what: str, name: str, t, dtype, shape, dev: int):
+    """Address of a contiguous tensor after checking its type, shape and
+    device (dev: a CUDA device index)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(what, f"{name}: expected contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}"
+                      f" with strides {t.stride()}")
+    if t.get_device() != dev:
+        _refuse(what, f"{name} is on {t.device}, not on CUDA device {dev}")
+    return t.data_ptr()
+
+
+def _rows(what: str, name: str, t, dtype, T: int, C: int, dev: int):
+    """Address and row stride of a [T, C] tensor whose rows are contiguous."""
+    if t.dtype is not dtype or t.shape != (T, C) or (C > 1 and T > 0 and t.stride(1) != 1):
+        _refuse(what, f"{name}: expected {dtype} ({T}, {C}) with contiguous rows, got {t.dtype} {tuple(t.shape)}"
+                      f" with strides {t.stride()}")
+    if t.get_device() != dev:
+        _refuse(what, f"{name} is on {t.device}, not on CUDA device {dev}")
+    return t.data_ptr(), (t.stride(0) if T > 1 else C)
+
+
+def _device(what: str, name: str, t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        _refuse(what, f"{name} is on {t.device}, not on a CUDA device")
+    return dev
+
+
+def _call(fn, what: str, dev: int, stream, *args):
+    """fn(*args, stream) with dev current; stream: dev's current one if None."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev == torch.cuda.current_device():
+        _check(fn(*args, s), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, s), what)
 
 
 # ------------------------------------------------------------------ sizes
@@ -483,9 +540,146 @@ def moe_combine_rows(y, rows, routed_scaling, out_f32, out_bf16, ws, stream=None
                                   _p(ws), ws.numel() * ws.element_size(), _s(stream)), "moe_combine_rows")
 
 
+# ------------------------------------------------ router losses and gradient
+
+def moe_balance_loss_workspace_bytes(T: int, E: int) -> int:
+    return int(lib().moe_balance_loss_workspace_bytes(T, E))
+
+
+def moe_balance_loss(logits, expert_offsets, loss, counts, prob_mean, ws, stream=None):
+    """Balance loss and z loss of a routed batch: logits [T, E] FP32 and
+    moe_route's expert_offsets [E+1] -> loss [2] FP32 (balance, z), counts
+    [E+1] int32 (pairs per expert, then the counted tokens) and prob_mean [E]."""
+    what = "moe_balance_loss"
+    T, E = logits.shape
+    dev = _device(what, "logits", logits)
+    f32, i32 = torch.float32, torch.int32
+    _call(lib().moe_balance_loss, what, dev, stream, _arg(what, "logits", logits, f32, (T, E), dev), T, E,
+          _arg(what, "expert_offsets", expert_offsets, i32, (E + 1,), dev), _arg(what, "loss", loss, f32, (2,), dev),
+          _arg(what, "counts", counts, i32, (E + 1,), dev), _arg(what, "prob_mean", prob_mean, f32, (E,), dev),
+          _arg(what, "ws", ws, ws.dtype, ws.shape, dev), ws.numel() * ws.element_size())
+
+
+def moe_route_backward(logits, topk_ids, topk_w, y, dout, routed_scaling, counts, d_loss, d_logits, stream=None):
+    """Gradient of the routing in the logits -> d_logits [T, E] FP32.  y
+    [T, k, H] FP32 slot rows (moe_grouped_ffn) with dout [T, H] BF16, the
+    gradient of the combined rows, give the part through the routing weights;
+    counts (moe_balance_loss) with d_loss [2] FP32 that of the balance and z
+    losses.  Either pair may be None."""
+    what = "moe_route_backward"
+    T, E = logits.shape
+    dev = _device(what, "logits", logits)
+    f32, i32 = torch.float32, torch.int32
+    k = H = 0
+    p_ids = p_w = p_y = p_dout = p_counts = p_loss = None
+    if y is not None:
+        _, k, H = y.shape
+        p_ids = _arg(what, "topk_ids", topk_ids, i32, (T, k), dev)
+        p_w = _arg(what, "topk_w", topk_w, f32, (T, k), dev)
+        p_y = _arg(what, "y", y, f32, (T, k, H), dev)
+        p_dout = _arg(what, "dout", dout, torch.bfloat16, (T, H), dev)
+    if d_loss is not None:
+        p_counts = _arg(what, "counts", counts, i32, (E + 1,), dev)
+        p_loss = _arg(what, "d_loss", d_loss, f32, (2,), dev)
+    elif y is None:
+        _refuse(what, "neither y nor d_loss is given")
+    elif T == 0:
+        return
+    _call(lib().moe_route_backward, what, dev, stream, _arg(what, "logits", logits, f32, (T, E), dev), T, E, p_ids,
+          p_w, k, p_y, p_dout, H, float(routed_scaling), p_counts, p_loss,
+          _arg(what, "d_logits", d_logits, f32, (T, E), dev))
+
+
+# ------------------------------------------------------- low-rank adapters
+
+def moe_lora(x, lora_a, lora_b, scales, adapter_offsets, sorted_tokens, base, v, out, out_bf16=None, stream=None):
+    """out[t] = base[t] + scales[a] * lora_b[a]^T (lora_a[a] x[t]) for the
+    tokens of every adapter a, grouped by moe_permute on [T, 1] adapter ids.
+    x [T, K] BF16; lora_a [n, rank, K] and lora_b [n, rank, N] BF16; scales
+    [n] FP32 or None; base [T, N] FP32, None (0) or out itself; v [T, rank]
+    FP32 (kept for the backward call); out [T, N] FP32; out_bf16 [T, N] or
+    None.  x, base and out may have strided rows."""
+    what = "moe_lora"
+    T, K = x.shape
+    n, R, N = lora_b.shape
+    dev = _device(what, "x", x)
+    f32, i32, b16 = torch.float32, torch.int32, torch.bfloat16
+    p_x, ld_x = _rows(what, "x", x, b16, T, K, dev)
+    p_out, ld_out = _rows(what, "out", out, f32, T, N, dev)
+    p_base, ld_base = (None, 0) if base is None else _rows(what, "base", base, f32, T, N, dev)
+    _call(lib().moe_lora, what, dev, stream, p_x, ld_x, T, K, _arg(what, "lora_a", lora_a, b16, (n, R, K), dev),
+          _arg(what, "lora_b", lora_b, b16, (n, R, N), dev),
+          None if scales is None else _arg(what, "scales", scales, f32, (n,), dev), n, R, N,
+          _arg(what, "adapter_offsets", adapter_offsets, i32, (n + 1,), dev),
+          _arg(what, "sorted_tokens", sorted_tokens, i32, (T,), dev), p_base, ld_base,
+          _arg(what, "v", v, f32, (T, R), dev), p_out, ld_out,
+          None if out_bf16 is None else _arg(what, "out_bf16", out_bf16, b16, (T, N), dev))
+
+
+def moe_lora_backward_workspace_bytes(T: int, rank: int) -> int:
+    return int(lib().moe_lora_backward_workspace_bytes(T, rank))
+
+
+def moe_lora_backward(x, lora_a, lora_b, scales, adapter_offsets, sorted_tokens, v, dout, dx_base, dx, d_a, d_b, ws,
+                      stream=None):
+    """Gradients of moe_lora for dout [T, N] BF16: dx [T, K] FP32 (dx_base
+    plus the adapters' part, for tokens with an adapter; None: not wanted),
+    d_a [n, rank, K] and d_b [n, rank, N] FP32.  v as moe_lora wrote it."""
+    what = "moe_lora_backward"
+    T, K = x.shape
+    n, R, N = lora_b.shape
+    dev = _device(what, "x", x)
+    f32, i32, b16 = torch.float32, torch.int32, torch.bfloat16
+    p_x, ld_x = _rows(what, "x", x, b16, T, K, dev)
+    p_dout, ld_dout = _rows(what, "dout", dout, b16, T, N, dev)
+    p_dx, ld_dx = (None, 0) if dx is None else _rows(what, "dx", dx, f32, T, K, dev)
+    p_base, ld_base = (None, 0) if dx_base is None else _rows(what, "dx_base", dx_base, f32, T, K, dev)
+    _call(lib().moe_lora_backward, what, dev, stream, p_x, ld_x, T, K,
+          _arg(what, "lora_a", lora_a, b16, (n, R, K), dev), _arg(what, "lora_b", lora_b, b16, (n, R, N), dev),
+          None if scales is None else _arg(what, "scales", scales, f32, (n,), dev), n, R, N,
+          _arg(what, "adapter_offsets", adapter_offsets, i32, (n + 1,), dev),
+          _arg(what, "sorted_tokens", sorted_tokens, i32, (T,), dev), _arg(what, "v", v, f32, (T, R), dev), p_dout,
+          ld_dout, p_base, ld_base, p_dx, ld_dx, _arg(what, "d_a", d_a, f32, (n, R, K), dev),
+          _arg(what, "d_b", d_b, f32, (n, R, N), dev), _arg(what, "ws", ws, ws.dtype, ws.shape, dev),
+          ws.numel() * ws.element_size())
+
+
 # ------------------------------------------------------------------ layer
 
-class RoutedMoE:
+class _RouterGradient:
+    """The router's losses and gradient of a layer class, from the routing
+    and slot rows that its last forward call left in its buffers."""
+
+    def balance_loss(self, logits: torch.Tensor, stream=None):
+        """(loss [2], counts [E+1]) of the batch that forward routed last:
+        balance and z loss, pairs per expert and counted tokens."""
+        T = logits.shape[0]
+        assert T <= self.max_tokens and logits.shape == (T, self.E)
+        if getattr(self, "loss", None) is None:
+            dev = self.offsets.device
+            self.loss = torch.empty((2,), dtype=torch.float32, device=dev)
+            self.counts = torch.empty((self.E + 1,), dtype=torch.int32, device=dev)
+            self.prob_mean = torch.empty((self.E,), dtype=torch.float32, device=dev)
+            self.ws_loss = torch.empty((moe_balance_loss_workspace_bytes(self.max_tokens, self.E),),
+                                       dtype=torch.uint8, device=dev)
+        moe_balance_loss(logits, self.offsets, self.loss, self.counts, self.prob_mean, self.ws_loss, stream)
+        return self.loss, self.counts
+
+    def router_backward(self, logits: torch.Tensor, dout, d_loss=None, d_logits=None, stream=None) -> torch.Tensor:
+        """d_logits [T, E] for dout [T, H] BF16 (the gradient of forward's
+        rows; None: not through the routing weights) and d_loss [2] FP32 (of
+        balance_loss's terms; None: without them)."""
+        T = logits.shape[0]
+        assert T <= self.max_tokens and logits.shape == (T, self.E)
+        assert d_loss is None or getattr(self, "counts", None) is not None, "balance_loss comes first"
+        if d_logits is None:
+            d_logits = torch.empty((T, self.E), dtype=torch.float32, device=logits.device)
+        moe_route_backward(logits, self.ids[:T], self.tw[:T], None if dout is None else self.y[:T], dout, self.rs,
+                           None if d_loss is None else self.counts, d_loss, d_logits, stream)
+        return d_logits
+
+
+class RoutedMoE(_RouterGradient):
     """One routed-expert layer: resident FP8 weights and their block scales,
     plus output and workspace buffers sized for up to `max_tokens` rows.
     ``forward`` enqueues moe_route_quant (or, with fused=False, moe_quant_act
@@ -515,8 +709,9 @@ class RoutedMoE:
         self.ws_comb = torch.empty((moe_combine_workspace_bytes(),), dtype=u8, device=dev)
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, out_bf16: torch.Tensor | None = None,
-                stream=None, stage_events=None, fused: bool = True) -> torch.Tensor:
-        """stage_events: None, or 7 recorded torch.cuda.Events marking the
+                stream=None, stage_events=None, fused: bool = True, adapters=None, batch=None) -> torch.Tensor:
+        """adapters, batch: a LoraAdapters (H to H) and the LoraBatch of
+        these tokens, whose rows are added to the layer's.  stage_events: None, or 7 recorded torch.cuda.Events marking the
         start of quantise, route, gather, gate/up, down, combine and the end
         (fused: the first two both mark the start of moe_route_quant)."""
         T = x.shape[0]
@@ -540,6 +735,8 @@ class RoutedMoE:
         moe_grouped_ffn(codes, scales, ids, tw, self.offsets, srt, *self.w, y, self.ws_ffn, stream,
                         stage_events=None if ev is None else ev[2:6])
         moe_combine(y, ids, self.E, self.rs, out, out_bf16, self.ws_comb, stream)
+        if adapters is not None:
+            adapters.forward(batch, x, out, out, out_bf16, stream)
         if ev is not None:
             ev[6].record(s)
         return out
@@ -549,7 +746,7 @@ class RoutedMoE:
                 | moe_get_device_status(self.ws_comb))
 
 
-class RoutedMoEMX:
+class RoutedMoEMX(_RouterGradient):
     """One routed-expert layer of the MXFP8 variant: resident E4M3 weights
     with UE8M0 scales per 32 values (packed once by moe_mx_pack_scales at
     construction), buffers for up to `max_tokens` rows.  ``forward`` enqueues
@@ -580,8 +777,8 @@ class RoutedMoEMX:
         self.ws_comb = torch.empty((moe_combine_workspace_bytes(),), dtype=u8, device=dev)
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, out_bf16: torch.Tensor | None = None,
-                stream=None, stage_events=None) -> torch.Tensor:
-        """stage_events: None, or 6 recorded torch.cuda.Events marking the
+                stream=None, stage_events=None, adapters=None, batch=None) -> torch.Tensor:
+        """adapters, batch: as RoutedMoE.forward.  stage_events: None, or 6 recorded torch.cuda.Events marking the
         start of quantise + route, gather, gate/up, down, combine and the end."""
         T = x.shape[0]
         assert T <= self.max_tokens and x.shape[1] == self.H and logits.shape == (T, self.E)
@@ -597,6 +794,8 @@ class RoutedMoEMX:
         moe_grouped_ffn_mx(codes, scales, ids, tw, self.offsets, srt, *self.w, y, self.ws_ffn, stream,
                            stage_events=None if ev is None else ev[1:5])
         moe_combine(y, ids, self.E, self.rs, out, out_bf16, self.ws_comb, stream)
+        if adapters is not None:
+            adapters.forward(batch, x, out, out, out_bf16, stream)
         if ev is not None:
             ev[5].record(s)
         return out

@@ -385,6 +385,136 @@ int moe_combine_rows(const float* y, int64_t y_nrows, const int32_t* rows, int64
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_combine_rows");
 }
 
+size_t moe_balance_loss_workspace_bytes(int64_t T, int E)
+{
+    if (T < 0 || E < 1) return 0;
+    size_t a, b;
+    return balance_ws_layout(T, E, &a, &b);
+}
+
+int moe_balance_loss(const float* logits, int64_t T, int E, const int32_t* expert_offsets, float* loss,
+                     int32_t* counts, float* prob_mean, void* ws, size_t ws_bytes, void* stream)
+{
+    if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS) return MOE_ERR_INVALID_ARG;
+    if (T > (int64_t(1) << 31) - 1) return MOE_ERR_UNSUPPORTED;
+    if (!expert_offsets || !loss || !counts || !prob_mean || !ws || (T > 0 && !logits)) return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {logits, expert_offsets, loss, counts, prob_mean, ws};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    if (ws_bytes < moe_balance_loss_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
+    if (int r = check_device()) return r;
+    cudaError_t err = launch_balance_loss(logits, T, E, expert_offsets, loss, counts, prob_mean, ws,
+                                          static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_balance_loss");
+}
+
+int moe_route_backward(const float* logits, int64_t T, int E, const int32_t* topk_ids, const float* topk_w, int top_k,
+                       const float* y, const uint16_t* dout, int H, float routed_scaling, const int32_t* counts,
+                       const float* d_loss, float* d_logits, void* stream)
+{
+    if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS) return MOE_ERR_INVALID_ARG;
+    if (!y && !d_loss) return MOE_ERR_INVALID_ARG;
+    if (y && (top_k < 1 || top_k > MOE_MAX_TOP_K || H < 128 || H > MOE_MAX_HIDDEN || H % 128 != 0))
+        return MOE_ERR_INVALID_ARG;
+    if (T > ((int64_t(1) << 31) - 1) / (y ? top_k : 1)) return MOE_ERR_UNSUPPORTED;
+    if (T > 0 && (!logits || !d_logits)) return MOE_ERR_INVALID_ARG;
+    if (y && T > 0 && (!topk_ids || !topk_w || !dout)) return MOE_ERR_INVALID_ARG;
+    if (d_loss && !counts) return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {logits, topk_ids, topk_w, y, dout, counts, d_logits};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    if (reinterpret_cast<uintptr_t>(d_loss) & 3u) return MOE_ERR_ALIGNMENT;
+    if (T == 0) return MOE_OK;
+    if (int r = check_device()) return r;
+    const RouteGradArgs a{logits, T,  E,   topk_ids,       topk_w, y ? top_k : 0, y,
+                          dout,   H, routed_scaling, counts, d_loss, d_logits};
+    cudaError_t err = launch_route_grad(a, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_route_backward");
+}
+
+}  // extern "C"
+
+namespace {
+
+bool row_major(int64_t ld, int cols, int unit) { return ld >= cols && ld % unit == 0; }
+
+// Sizes shared by the adapter entry points.
+int lora_check(int64_t T, int K, int N, int n_adapters, int rank)
+{
+    if (T < 0 || K < 8 || K > MOE_MAX_HIDDEN || N < 8 || N > MOE_MAX_HIDDEN) return MOE_ERR_INVALID_ARG;
+    if (n_adapters < 1 || n_adapters > MOE_MAX_EXPERTS || rank < 1 || rank > MOE_MAX_LORA_RANK)
+        return MOE_ERR_INVALID_ARG;
+    if (K % 8 != 0 || N % 8 != 0) return MOE_ERR_UNSUPPORTED;  // rows are read in 16-byte pieces
+    // grids and sorted places are 32-bit
+    if (T > (int64_t(1) << 24)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_lora(const uint16_t* x, int64_t ld_x, int64_t T, int K, const uint16_t* lora_a, const uint16_t* lora_b,
+             const float* scales, int n_adapters, int rank, int N, const int32_t* adapter_offsets,
+             const int32_t* sorted_tokens, const float* base, int64_t ld_base, float* v, float* out, int64_t ld_out,
+             uint16_t* out_bf16, void* stream)
+{
+    if (int r = lora_check(T, K, N, n_adapters, rank)) return r;
+    if (!row_major(ld_x, K, 8) || !row_major(ld_out, N, 4) || (base && !row_major(ld_base, N, 4)))
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!x || !lora_a || !lora_b || !adapter_offsets || !sorted_tokens || !v || !out))
+        return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {x, lora_a, lora_b, scales, adapter_offsets, sorted_tokens, base, v, out, out_bf16};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    if (T == 0) return MOE_OK;
+    if (int r = check_device()) return r;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const LoraRows rows{T, n_adapters, adapter_offsets, sorted_tokens};
+    cudaError_t err = launch_lora_shrink(rows, x, ld_x, K, lora_a, rank, nullptr, v, s);
+    if (err == cudaSuccess)
+        err = launch_lora_expand(rows, v, rank, lora_b, N, scales, base, ld_base, out, ld_out, out_bf16, s);
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_lora");
+}
+
+size_t moe_lora_backward_workspace_bytes(int64_t T, int rank)
+{
+    if (T < 0 || rank < 1) return 0;
+    return align_up(static_cast<size_t>(T > 0 ? T : 1) * rank * 4, 256);
+}
+
+int moe_lora_backward(const uint16_t* x, int64_t ld_x, int64_t T, int K, const uint16_t* lora_a,
+                      const uint16_t* lora_b, const float* scales, int n_adapters, int rank, int N,
+                      const int32_t* adapter_offsets, const int32_t* sorted_tokens, const float* v,
+                      const uint16_t* dout, int64_t ld_dout, const float* dx_base, int64_t ld_dx_base, float* dx,
+                      int64_t ld_dx, float* d_a, float* d_b, void* ws, size_t ws_bytes, void* stream)
+{
+    if (int r = lora_check(T, K, N, n_adapters, rank)) return r;
+    if (!row_major(ld_x, K, 8) || !row_major(ld_dout, N, 8) || (dx && !row_major(ld_dx, K, 4)) ||
+        (dx_base && !row_major(ld_dx_base, K, 4)))
+        return MOE_ERR_INVALID_ARG;
+    if (!d_a || !d_b || !adapter_offsets || !ws) return MOE_ERR_INVALID_ARG;
+    if (dx_base && !dx) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!x || !lora_a || !lora_b || !sorted_tokens || !v || !dout)) return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {x, lora_a, lora_b, scales, adapter_offsets, sorted_tokens, v, dout, dx_base, dx, d_a, d_b,
+                          ws};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    if (ws_bytes < moe_lora_backward_workspace_bytes(T, rank)) return MOE_ERR_WORKSPACE;
+    if (int r = check_device()) return r;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const LoraRows rows{T, n_adapters, adapter_offsets, sorted_tokens};
+    float* dv = static_cast<float*>(ws);
+    cudaError_t err = cudaSuccess;
+    if (T > 0) err = launch_lora_shrink(rows, dout, ld_dout, N, lora_b, rank, scales, dv, s);
+    if (err == cudaSuccess && T > 0 && dx)
+        err = launch_lora_expand(rows, dv, rank, lora_a, K, nullptr, dx_base, ld_dx_base, dx, ld_dx, nullptr, s);
+    if (err == cudaSuccess)
+        err = launch_lora_outer(rows, rank, LoraOuter{dv, x, ld_x, K, nullptr, d_a},
+                                LoraOuter{v, dout, ld_dout, N, scales, d_b}, s);
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_lora_backward");
+}
+
 int moe_get_device_status(const void* ws, int* status_out)
 {
     if (!ws || !status_out) return MOE_ERR_INVALID_ARG;

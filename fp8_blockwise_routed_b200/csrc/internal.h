@@ -186,4 +186,55 @@ size_t ffn_mx_workspace_layout(int64_t T, int H, int I, int k, size_t* off_a, si
                                size_t* off_sh);
 cudaError_t launch_grouped_ffn_mx(const FfnMxArgs& a, cudaStream_t s);
 
+// Balance loss: at most this many blocks sum the probabilities (two per SM
+// of a B200), so the partial sums and their order do not depend on T beyond it.
+constexpr int kLossMaxBlocks = 296;
+// Workspace: FP64 lse^2 sums, token counts, probability sums [blocks, E].
+size_t balance_ws_layout(int64_t T, int E, size_t* off_n, size_t* off_part);
+cudaError_t launch_balance_loss(const float* logits, int64_t T, int E, const int32_t* offsets, float* loss,
+                                int32_t* counts, float* prob_mean, void* ws, cudaStream_t s);
+
+struct RouteGradArgs {
+    const float* logits;
+    int64_t T;
+    int E;
+    const int32_t* ids;    // [T, k]
+    const float* w;        // [T, k]
+    int k;
+    const float* y;        // nullable: [T, k, H]
+    const uint16_t* dout;  // [T, H] BF16
+    int H;
+    float rs;
+    const int32_t* counts;  // [E + 1]
+    const float* d_loss;    // nullable: [2]
+    float* d_logits;        // [T, E]
+};
+cudaError_t launch_route_grad(const RouteGradArgs& a, cudaStream_t s);
+
+// Low-rank adapters.  A "pass" over the rows of one batch: rows are grouped
+// by adapter (offsets [n + 1], tokens sorted by adapter).
+struct LoraRows {
+    int64_t T;
+    int n;                   // adapters
+    const int32_t* offsets;  // [n + 1]
+    const int32_t* tokens;   // [T] sorted tokens
+};
+// v[p, r] = f_a * sum_c x[tok(p), c] w[a, r, c]   (f_a = scales[a] or 1)
+cudaError_t launch_lora_shrink(const LoraRows& rows, const uint16_t* x, int64_t ldx, int C, const uint16_t* w, int R,
+                               const float* scales, float* v, cudaStream_t s);
+// out[t, c] = base[t, c] + f_a * sum_r v[p, r] w[a, r, c]
+cudaError_t launch_lora_expand(const LoraRows& rows, const float* v, int R, const uint16_t* w, int C,
+                               const float* scales, const float* base, int64_t ld_base, float* out, int64_t ld_out,
+                               uint16_t* out_bf16, cudaStream_t s);
+// d[a, r, c] = f_a * sum_p v[p, r] x[tok(p), c], two such products at once
+struct LoraOuter {
+    const float* v;
+    const uint16_t* x;
+    int64_t ldx;
+    int C;
+    const float* scales;
+    float* d;
+};
+cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, const LoraOuter& b, cudaStream_t s);
+
 }  // namespace fp8moe

@@ -90,6 +90,7 @@ typedef enum {
 #define MOE_MAX_TOP_K 32
 #define MOE_MAX_INTERMEDIATE 8192
 #define MOE_MAX_HIDDEN 16384
+#define MOE_MAX_LORA_RANK 128
 
 /* Human-readable name of a moe_status value (static string). */
 MOE_API const char* moe_status_string(int status);
@@ -464,6 +465,127 @@ MOE_API int moe_grouped_ffn_rows(const uint8_t* codes, const float* act_scales, 
 MOE_API int moe_combine_rows(const float* y, int64_t y_nrows, const int32_t* rows, int64_t T, int H, int top_k,
                              float routed_scaling, float* out_f32, uint16_t* out_bf16, void* ws, size_t ws_bytes,
                              void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_balance_loss -- the router's balance loss and z loss over a batch, with
+ * per-expert counts.  The pages describe inference only; the definitions are
+ * the usual ones of routed layers.  For logits z [T, E] that moe_route (or
+ * moe_route_shared) routed:
+ *   p[t, e] = softmax of row t over its selectable logits (not NaN, not
+ *             -Inf), 0 at the others; a row without any is not counted;
+ *   N       = number of counted rows;  c[e] = expert_offsets[e+1] -
+ *             expert_offsets[e];  P = expert_offsets[E];
+ *   loss[0] = E * sum_e (c[e] / P) * (1/N) sum_t p[t, e]   (1 when uniform);
+ *   loss[1] = (1/N) sum_t (log sum_e exp z[t, e])^2;
+ * both 0 when nothing is counted.  A +Inf logit gives NaN, as it does in the
+ * routing weights.
+ *
+ *   logits          [T, E]   FP32, read
+ *   expert_offsets  [E + 1]  int32, read (moe_route output)
+ *   loss            [2]      FP32, written
+ *   counts          [E + 1]  int32, written: c[0..E-1], then N
+ *   prob_mean       [E]      FP32, written: (1/N) sum_t p[t, e]
+ *   ws, ws_bytes    scratch of at least moe_balance_loss_workspace_bytes(T, E)
+ *
+ * The sums over rows have a fixed order (FP32 inside a block, FP64 across
+ * blocks): the same bits on every call.  The call records no device status.
+ * Limits: T >= 0, 1 <= E <= 1024.
+ * ------------------------------------------------------------------------- */
+MOE_API size_t moe_balance_loss_workspace_bytes(int64_t T, int E);
+MOE_API int moe_balance_loss(const float* logits, int64_t T, int E, const int32_t* expert_offsets, float* loss,
+                             int32_t* counts, float* prob_mean, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_route_backward -- the gradient of the routing in the logits: that of
+ * the layer's output through the routing weights, plus d_loss[0] and
+ * d_loss[1] times those of moe_balance_loss's two terms.  With s[t, j] =
+ * routed_scaling * <dout[t], y[t, j]> over the slots with an id in [0, E):
+ *   d_logits[t, e] = sum_{j: id(t,j) = e} (s[t, j] - topk_w[t, j] * sum_i s[t, i])
+ *       + p[t, e] * (g[e] - sum_e' p[t, e'] g[e'] + 2 d_loss[1] lse[t] / N),
+ *   g[e] = d_loss[0] * E * c[e] / (P * N),  P = sum_e c[e].
+ * y already carries the routing weight, so nothing is divided by it; the
+ * counts are constants of the gradient.  A caller that balances over several
+ * ranks sums counts over them before this call.  Every row of d_logits is
+ * written; logits that are not selectable get 0.  Slots whose id is outside
+ * [0, E) (unfilled, or the shared expert's) are skipped and their rows of y
+ * not read.
+ *
+ *   logits            [T, E]  FP32, read
+ *   topk_ids, topk_w  [T, top_k] int32 / FP32, read (moe_route output)
+ *   y                 [T, top_k, H] FP32, read (moe_grouped_ffn output), or
+ *                     NULL: no gradient through the routing weights (then
+ *                     topk_ids, topk_w, top_k, dout, H are not used)
+ *   dout              [T, H]  BF16 words, read: the gradient of moe_combine's rows
+ *   counts            [E + 1] int32, read (moe_balance_loss output)
+ *   d_loss            [2]     FP32 on the device, read, or NULL: no balance
+ *                     terms (then counts is not used); y or d_loss is given
+ *   d_logits          [T, E]  FP32, written; must not overlap logits
+ *
+ * Limits: as moe_combine and moe_balance_loss.  The call needs no workspace
+ * and records no device status.
+ * ------------------------------------------------------------------------- */
+MOE_API int moe_route_backward(const float* logits, int64_t T, int E, const int32_t* topk_ids, const float* topk_w,
+                               int top_k, const float* y, const uint16_t* dout, int H, float routed_scaling,
+                               const int32_t* counts, const float* d_loss, float* d_logits, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_lora -- low-rank adapters of many requests beside a projection that
+ * they share (the shared expert's, or the whole routed layer's).  Tokens are
+ * grouped by adapter exactly as pairs are by expert: moe_permute on ids
+ * [T, 1] (-1: no adapter) with E = n_adapters gives adapter_offsets and
+ * sorted_tokens, once per batch for every projection the batch passes.  For
+ * place p of sorted_tokens, t = sorted_tokens[p], adapter a:
+ *   v[p, r]   = sum_c x[t, c] lora_a[a, r, c]
+ *   out[t, c] = base[t, c] + scales[a] * sum_r v[p, r] lora_b[a, r, c]
+ * with exact BF16 products summed in FP32 and v kept in FP32.  Rows of
+ * tokens without an adapter are left as they were, as are rows of v at and
+ * past adapter_offsets[n_adapters].  A row's bits depend on its adapter's
+ * weights and its own inputs only, for one T, n_adapters and rank.
+ *
+ *   x               [T, K] BF16 words, row stride ld_x elements, read
+ *   lora_a          [n_adapters, rank, K] BF16 words, read
+ *   lora_b          [n_adapters, rank, N] BF16 words, read: rank-major, the
+ *                   transpose of an output projection's [N, rank]
+ *   scales          [n_adapters] FP32, read, or NULL (1)
+ *   adapter_offsets [n_adapters + 1] int32, read
+ *   sorted_tokens   [T] int32, read (entries outside [0, T) are skipped)
+ *   base            [T, N] FP32, row stride ld_base, read, or NULL (0); may
+ *                   be out itself (the product is then added in place)
+ *   v               [T, rank] FP32, written (kept for moe_lora_backward)
+ *   out             [T, N] FP32, row stride ld_out, written: for instance a
+ *                   shared-expert slot of y (ld_out = (top_k + 1) * H)
+ *   out_bf16        [T, N] BF16 words, contiguous, written, nullable
+ *
+ * Limits: T >= 0 (at most 2^24); 1 <= n_adapters <= 1024; 1 <= rank <= 128;
+ * K, N multiples of 8, 8 .. 16384; ld_x a multiple of 8, ld_base and ld_out
+ * of 4.  No workspace, no device status.
+ *
+ * moe_lora_backward -- its gradients, for dout the gradient of out:
+ *   dv[p, r]     = scales[a] * sum_c dout[t, c] lora_b[a, r, c]
+ *   dx[t, c]     = dx_base[t, c] + sum_r dv[p, r] lora_a[a, r, c]
+ *   d_a[a, r, c] = sum_p dv[p, r] x[t, c]
+ *   d_b[a, r, c] = scales[a] * sum_p v[p, r] dout[t, c]
+ *
+ *   v           [T, rank] FP32, read (moe_lora output of the same rows)
+ *   dout        [T, N] BF16 words, row stride ld_dout (multiple of 8), read
+ *   dx_base     [T, K] FP32, row stride ld_dx_base, read, or NULL (0); may be dx
+ *   dx          [T, K] FP32, row stride ld_dx, written for tokens with an
+ *               adapter, or NULL: no gradient of x
+ *   d_a, d_b    [n_adapters, rank, K] and [n_adapters, rank, N] FP32, written
+ *               in full (zeros for an adapter without tokens)
+ *   ws          scratch of at least moe_lora_backward_workspace_bytes(T, rank)
+ * ------------------------------------------------------------------------- */
+MOE_API int moe_lora(const uint16_t* x, int64_t ld_x, int64_t T, int K, const uint16_t* lora_a,
+                     const uint16_t* lora_b, const float* scales, int n_adapters, int rank, int N,
+                     const int32_t* adapter_offsets, const int32_t* sorted_tokens, const float* base,
+                     int64_t ld_base, float* v, float* out, int64_t ld_out, uint16_t* out_bf16, void* stream);
+MOE_API size_t moe_lora_backward_workspace_bytes(int64_t T, int rank);
+MOE_API int moe_lora_backward(const uint16_t* x, int64_t ld_x, int64_t T, int K, const uint16_t* lora_a,
+                              const uint16_t* lora_b, const float* scales, int n_adapters, int rank, int N,
+                              const int32_t* adapter_offsets, const int32_t* sorted_tokens, const float* v,
+                              const uint16_t* dout, int64_t ld_dout, const float* dx_base, int64_t ld_dx_base,
+                              float* dx, int64_t ld_dx, float* d_a, float* d_b, void* ws, size_t ws_bytes,
+                              void* stream);
 
 /* ---------------------------------------------------------------------------
  * moe_layer -- the whole routed-expert layer in one call: moe_route_quant,
