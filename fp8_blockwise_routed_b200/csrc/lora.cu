@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "sm100.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -48,23 +49,44 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// a = h + m + l in BF16 terms; h alone where a is not finite or rounds to
-// infinity, so that no Inf - Inf turns an infinity into NaN.
-struct Split {
-    float h, m, l;
-};
-__device__ __forceinline__ Split split3(float a)
+// a = h + m + l in BF16 terms, two neighbours at a time; h alone where a is
+// not finite or rounds to infinity, so that no Inf - Inf makes a NaN of it.
+__device__ __forceinline__ void split3_pair(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l)
 {
-    Split s;
-    s.h = __bfloat162float(__float2bfloat16_rn(a));
-    const bool fin = fabsf(s.h) <= 3.4028234e38f;
-    const float r = fin ? a - s.h : 0.0f;
-    s.m = __bfloat162float(__float2bfloat16_rn(r));
-    s.l = r - s.m;
-    return s;
+    h = pack_bf16(a, b);
+    const float ha = __uint_as_float(h << 16), hb = __uint_as_float(h & 0xFFFF0000u);
+    float ra = fabsf(ha) <= 3.4028234e38f ? a - ha : 0.0f;
+    float rb = fabsf(hb) <= 3.4028234e38f ? b - hb : 0.0f;
+    m = pack_bf16(ra, rb);
+    ra -= __uint_as_float(m << 16);
+    rb -= __uint_as_float(m & 0xFFFF0000u);
+    l = pack_bf16(ra, rb);
 }
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+// 16 bytes from global to shared memory without registers; zeros if !in
+// (then nothing is read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Programmatic launch: a kernel of a call lets the next one start its blocks
+// (which load what does not depend on it) and that one waits here until
+// everything before it in the stream is complete and visible.
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The `tile`-th group of at most BT sorted tokens of one adapter, adapters in
 // order.  Called by the whole block; offsets are clamped to [0, T], so a
@@ -147,6 +169,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
     const int nc = static_cast<int>(cluster.num_blocks());
     const int rank = static_cast<int>(cluster.block_rank());
     const int64_t unit = blockIdx.x / nc;
+    allow_next();
     const Tile tile = find_tile<kShrinkThreads>(rows, kShrinkTokens, unit / rblocks);
     if (tile.a < 0) return;  // the whole cluster
     const int r0 = static_cast<int>(unit % rblocks) * MR * 16;
@@ -165,24 +188,30 @@ __global__ void __launch_bounds__(kShrinkThreads)
         for (int i = 0; i < 4; ++i) acc[m][i] = sum[m][i] = 0.0f;
     const int chunks = (C + 31) / 32;
     int since = 0;
-    for (int c = rank * (kShrinkThreads / 32) + warp; c < chunks; c += nc * (kShrinkThreads / 32)) {
-        const int k = c * 32 + q * 8;
-        const bool in = k < C;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        const uint4 b = (in && xr) ? ldg16(xr + k) : zero;
-        uint4 lo[MR], hi[MR];
+    const int step = nc * (kShrinkThreads / 32);
+    for (int c = rank * (kShrinkThreads / 32) + warp; c < chunks; c += 2 * step) {
+        uint4 b[2], lo[2][MR], hi[2][MR];
 #pragma unroll
-        for (int m = 0; m < MR; ++m) {
-            const int r = m * 16 + g;
-            lo[m] = (in && r0 + r < R) ? ldg16(wa + static_cast<int64_t>(r) * C + k) : zero;
-            hi[m] = (in && r0 + r + 8 < R) ? ldg16(wa + static_cast<int64_t>(r + 8) * C + k) : zero;
+        for (int u = 0; u < 2; ++u) {  // two column steps' loads in flight
+            const int k = (c + u * step) * 32 + q * 8;
+            const bool in = k < C;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            b[u] = (in && xr) ? ldg16(xr + k) : zero;
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                const int r = m * 16 + g;
+                lo[u][m] = (in && r0 + r < R) ? ldg16(wa + static_cast<int64_t>(r) * C + k) : zero;
+                hi[u][m] = (in && r0 + r + 8 < R) ? ldg16(wa + static_cast<int64_t>(r + 8) * C + k) : zero;
+            }
         }
 #pragma unroll
-        for (int m = 0; m < MR; ++m) {
-            mma_bf16(acc[m], lo[m].x, hi[m].x, lo[m].y, hi[m].y, b.x, b.y);
-            mma_bf16(acc[m], lo[m].z, hi[m].z, lo[m].w, hi[m].w, b.z, b.w);
-        }
-        if (++since == 8) {  // short chains on the tensor core, joined in FP32
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                mma_bf16(acc[m], lo[u][m].x, hi[u][m].x, lo[u][m].y, hi[u][m].y, b[u].x, b[u].y);
+                mma_bf16(acc[m], lo[u][m].z, hi[u][m].z, lo[u][m].w, hi[u][m].w, b[u].z, b[u].w);
+            }
+        if (++since == 4) {  // short chains on the tensor core, joined in FP32
             since = 0;
 #pragma unroll
             for (int m = 0; m < MR; ++m)
@@ -218,254 +247,650 @@ __global__ void __launch_bounds__(kShrinkThreads)
     cluster.sync();  // the peers have read this block's part
 }
 
+// The same product for adapters with many tokens: 128 tokens times all ranks
+// per cluster on tcgen05, the columns dealt to the cluster's blocks 64 at a
+// time.  A stage holds the 128 token rows and the RP rank rows of 64 columns
+// (128-byte rows, 128-byte swizzle, filled by cp.async, which gathers the
+// token rows and zero-fills what is missing); one thread issues the four MMAs
+// of a stage.  The accumulator is moved from TMEM to FP32 registers every
+// four stages (two TMEM buffers in turn), so a chain on the tensor core stays
+// 256 columns long.  At the end the blocks' sums are joined in block order.
+constexpr int kTileTokens = 128;
+constexpr int kTileThreads = 128;
+constexpr int kTileChain = 4;  // stages per accumulation chain
+constexpr uint64_t kTileWaitNs = 2000000000ull;
+
+constexpr int tile_stages(int RP) { return RP <= 64 ? 4 : 3; }
+constexpr int tile_stage_bytes(int RP) { return (kTileTokens + RP) * 128; }
+constexpr int tile_smem(int RP)
+{
+    return 1024 + tile_stages(RP) * tile_stage_bytes(RP);
+}
+constexpr uint32_t tile_acc(int RP) { return RP <= 32 ? 32 : RP; }  // TMEM columns of one accumulator
+constexpr uint32_t tile_tmem(int RP) { return 2 * tile_acc(RP); }
+
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor, kind::f16: D FP32, A and B BF16, dense, M x N;
+// a_mn / b_mn: that operand is MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kTileThreads)
+    lora_shrink_tile_kernel(LoraRows rows, const uint16_t* __restrict__ x, int64_t ldx, int C,
+                            const uint16_t* __restrict__ w, int R, const float* __restrict__ scales,
+                            float* __restrict__ v)
+{
+    constexpr int S = tile_stages(RP);
+    constexpr int kStage = tile_stage_bytes(RP);
+    constexpr int RL = (RP + 31) / 32 * 32;  // accumulator columns read
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(8) uint64_t s_bar[S];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ int s_tok[kTileTokens];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int nc = static_cast<int>(cluster.num_blocks());
+    const int rank = static_cast<int>(cluster.block_rank());
+    allow_next();
+    const Tile tile = find_tile<kTileThreads>(rows, kTileTokens, blockIdx.x / nc);
+    if (tile.a < 0) return;  // the whole cluster
+    uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    const uint32_t ring_s = sm100::smem_u32(ring);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) sm100::mbar_init(sm100::smem_u32(&s_bar[i]), 1);
+        sm100::fence_barrier_init();
+        s_abort = 0;
+    }
+    if (warp == 0) {
+        sm100::tmem_alloc(sm100::smem_u32(&s_tmem), tile_tmem(RP));
+        sm100::tmem_relinquish();
+    }
+    {
+        int tok = (tid < tile.count) ? __ldg(rows.tokens + tile.p0 + tid) : -1;
+        s_tok[tid] = (tok >= 0 && tok < rows.T) ? tok : -1;
+    }
+    sm100::tc_fence_before();
+    __syncthreads();
+    sm100::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const uint16_t* wa = w + static_cast<int64_t>(tile.a) * R * C;
+    const int ch = tid & 7, row0 = tid >> 3;
+    const int chunks = (C + 63) / 64;
+    const int mine = (chunks - rank + nc - 1) / nc;  // this block's: rank, rank + nc, ...
+    const uint32_t swz = (static_cast<uint32_t>(ch ^ (row0 & 7)) << 4);
+    auto load = [&](int i) {
+        if (i < mine) {
+            const int k = (rank + i * nc) * 64 + ch * 8;
+            const bool in = k < C;
+            const uint32_t dst = ring_s + (i % S) * kStage + row0 * 128 + swz;
+#pragma unroll
+            for (int j = 0; j < kTileTokens / 16; ++j) {
+                const int tok = s_tok[row0 + 16 * j];
+                const bool ok = in && tok >= 0;
+                cp_async16(dst + j * 2048, ok ? x + tok * ldx + k : x, ok);
+            }
+#pragma unroll
+            for (int j = 0; j < RP / 16; ++j) {
+                const int r = row0 + 16 * j;
+                const bool ok = in && r < R;
+                cp_async16(dst + kTileTokens * 128 + j * 2048, ok ? wa + static_cast<int64_t>(r) * C + k : w, ok);
+            }
+        }
+        cp_async_commit();
+    };
+    float sum[RL];
+#pragma unroll
+    for (int r = 0; r < RL; ++r) sum[r] = 0.0f;
+    bool alive = true;
+    auto wait_stage = [&](int i) {  // the MMAs of this block's i-th step are complete
+        alive = alive && sm100::mbar_wait_bounded(sm100::smem_u32(&s_bar[i % S]), (i / S) & 1,
+                                                  reinterpret_cast<volatile int*>(&s_abort), kTileWaitNs);
+    };
+    auto promote = [&](int chain) {
+        sm100::tc_fence_after();
+#pragma unroll
+        for (int c0 = 0; c0 < RL; c0 += 32) {
+            uint32_t t[32];
+            sm100::tmem_ld32_issue(tmem + (static_cast<uint32_t>(warp) << 21) + (chain & 1) * tile_acc(RP) + c0, t);
+            sm100::tmem_ld_wait(t);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) sum[c0 + u] += __uint_as_float(t[u]);
+        }
+        sm100::tc_fence_before();
+    };
+    for (int i = 0; i < S - 1; ++i) load(i);
+    constexpr uint32_t idesc = idesc_bf16_f32(kTileTokens, RP, 0, 0);
+    for (int i = 0; i < mine; ++i) {
+        cp_async_wait<S - 2>();
+        sm100::fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0 && alive) {
+            sm100::tc_fence_after();
+            const uint32_t st = ring_s + (i % S) * kStage;
+            const uint64_t da = sm100::sw128_kmajor_desc(st), db = sm100::sw128_kmajor_desc(st + kTileTokens * 128);
+            const uint32_t d = tmem + ((i / kTileChain) & 1) * tile_acc(RP);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_f16_ss(d, da + 2 * kk, db + 2 * kk, idesc, (i % kTileChain != 0 || kk != 0) ? 1u : 0u);
+            sm100::mma_commit(sm100::smem_u32(&s_bar[i % S]));
+        }
+        if (i > 0) {
+            wait_stage(i - 1);
+            if (i % kTileChain == 0) promote(i / kTileChain - 1);
+        }
+        load(i + S - 1);
+    }
+    wait_stage(mine - 1);
+    promote((mine - 1) / kTileChain);
+    cp_async_wait<0>();
+    __syncthreads();
+    if (warp == 0) {
+        sm100::tc_fence_after();
+        sm100::tmem_dealloc(tmem, tile_tmem(RP));
+    }
+    // the block's sums, rank-minor; a wait that ran out leaves NaN
+    constexpr int kPitch = RP + 1;
+    float* const part = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int r = 0; r < RP; ++r) part[tid * kPitch + r] = alive ? sum[r] : NAN;
+    cluster.sync();
+    const float f = scales ? __ldg(scales + tile.a) : 1.0f;
+    const int per = kTileTokens / nc;  // this block's token rows
+    for (int e = tid; e < per * RP; e += kTileThreads) {
+        const int row = rank * per + e / RP, r = e % RP;
+        if (row >= tile.count || r >= R) continue;
+        float s = 0.0f;
+        for (int b = 0; b < nc; ++b) s += cluster.map_shared_rank(part, b)[row * kPitch + r];
+        v[static_cast<int64_t>(tile.p0 + row) * R + r] = f * s;
+    }
+    cluster.sync();  // the peers have read this block's sums
+}
+
 // ------------------------------------------------------------------ expand
 //
 // out[t, c] = base[t, c] + f_a sum_r v[p, r] w[a, r, c].  A warp keeps the
 // adapter's ranks of 8 NW columns in registers (the B operand, two rank rows
-// interleaved per register) and walks over the tile's tokens, 16 at a time:
-// tokens are the rows of the MMA, so that a lane ends up with 2 NW
-// consecutive columns of two rows, read and written in 16-byte pieces.  The
-// split terms of v wait in shared memory in the order of the A operand.
+// interleaved per register) and walks over the tile's tokens, 16 at a time.
+// Tokens are the rows of the MMA; column g of its j-th tile is column
+// 32 (j / 4) + 4 g + j % 4, so that a lane ends up with 8 consecutive columns
+// per row.  The base rows of the next two groups are on their way to a
+// per-warp ring in shared memory meanwhile; the sum is formed there in place
+// and written out in whole row segments.  v waits in shared memory in FP32 and
+// is split as it is read (each warp for itself: the splits hide under the
+// MMAs, where preparing them once per block stood in front of them).
 constexpr int kExpandThreads = 128;
+constexpr int kExpandRing = 3;
+
+template <int NW>
+constexpr int expand_pitch()  // bytes of a ring row: 16 past a multiple of 128, so fragment reads do not collide
+{
+    return 32 * NW + 16;
+}
+template <int KS>
+constexpr int expand_v_pitch()  // bytes of a row of v: 64 past a multiple of 128, as two rows are read at once
+{
+    return KS == 1 ? 64 : 64 * KS + 64;
+}
+template <int KS, int NW, int BT>
+constexpr int expand_smem()
+{
+    return BT * expand_v_pitch<KS>() + (kExpandThreads / 32) * kExpandRing * 16 * expand_pitch<NW>();
+}
 
 template <int KS, int NW, int BT>
 __global__ void __launch_bounds__(kExpandThreads)
-    lora_expand_kernel(LoraRows rows, const float* __restrict__ v, int R, const uint16_t* __restrict__ w, int C,
-                       int cblocks, const float* __restrict__ scales, const float* base, int64_t ld_base, float* out,
+    lora_expand_kernel(LoraRows rows, const float* v, int R, const uint16_t* __restrict__ w, int C, int cblocks,
+                       const float* __restrict__ scales, const float* base, int64_t ld_base, float* out,
                        int64_t ld_out, uint16_t* __restrict__ out_bf16)
 {
-    __shared__ __align__(16) uint32_t frag[BT / 16][3][KS][32 * 4];
+    constexpr int P = expand_pitch<NW>();
+    constexpr int kPieces = 2 * NW;         // 16-byte pieces of a row segment
+    constexpr int kRowsAt = 32 / kPieces;   // rows a warp moves per instruction
+    extern __shared__ __align__(16) uint8_t dyn[];
+    constexpr int VP = expand_v_pitch<KS>();
     __shared__ int s_tok[BT];
+    allow_next();
     const Tile tile = find_tile<kExpandThreads>(rows, BT, blockIdx.x / cblocks);
-    if (tile.a < 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, q = lane & 3;
     const int c0 = (static_cast<int>(blockIdx.x % cblocks) * (kExpandThreads / 32) + warp) * 8 * NW;
-    // the adapter's slab: ranks 16 s + 4 q + i, columns c0 + NW g + j
-    uint32_t b[KS][NW][2];
-    {
-        const int c = c0 + NW * g;
-        const uint16_t* wa = w + static_cast<int64_t>(tile.a) * R * C + c;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            uint32_t rr[4][NW / 2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 16 * s + 4 * q + i;
-                const bool in = r < R && c < C;
-                if (NW == 8) {
-                    const uint4 u = in ? ldg16(wa + static_cast<int64_t>(r) * C) : make_uint4(0, 0, 0, 0);
-                    rr[i][0] = u.x;
-                    rr[i][1] = u.y;
-                    rr[i][NW / 2 - 2] = u.z;
-                    rr[i][NW / 2 - 1] = u.w;
-                } else {
-                    const uint2 u = in ? __ldg(reinterpret_cast<const uint2*>(wa + static_cast<int64_t>(r) * C))
-                                       : make_uint2(0, 0);
-                    rr[i][0] = u.x;
-                    rr[i][1] = u.y;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < NW; ++j) {
-                const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-                b[s][j][0] = __byte_perm(rr[0][j / 2], rr[1][j / 2], sel);
-                b[s][j][1] = __byte_perm(rr[2][j / 2], rr[3][j / 2], sel);
-            }
-        }
-    }
-    // split terms of v, four ranks of one token at a time
-    for (int idx = threadIdx.x; idx < BT * KS * 4; idx += kExpandThreads) {
-        const int i = idx / (KS * 4), r4 = idx % (KS * 4);
-        Split t[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int r = r4 * 4 + u;
-            const bool in = i < tile.count && r < R;
-            t[u] = split3(in ? __ldg(v + static_cast<int64_t>(tile.p0 + i) * R + r) : 0.0f);
-        }
-        const int at = (((i & 7) * 4 + (r4 & 3)) << 2) + ((i >> 3) & 1);
-        uint32_t* d = &frag[i >> 4][0][r4 >> 2][at];
-        d[0] = pack_bf16(t[0].h, t[1].h);
-        d[2] = pack_bf16(t[2].h, t[3].h);
-        d[KS * 128] = pack_bf16(t[0].m, t[1].m);
-        d[KS * 128 + 2] = pack_bf16(t[2].m, t[3].m);
-        d[2 * KS * 128] = pack_bf16(t[0].l, t[1].l);
-        d[2 * KS * 128 + 2] = pack_bf16(t[2].l, t[3].l);
-    }
+    if (tile.a < 0) return;
     for (int i = threadIdx.x; i < BT; i += kExpandThreads) {
-        int tok = (i < tile.count) ? __ldg(rows.tokens + tile.p0 + i) : -1;
+        const int tok = (i < tile.count) ? __ldg(rows.tokens + tile.p0 + i) : -1;
         s_tok[i] = (tok >= 0 && tok < rows.T) ? tok : -1;
     }
+    // the adapter's slab: ranks 16 s + 4 q + i, columns c0 + 32 h + 4 g + 0..3
+    uint32_t b[KS][NW][2];
+    {
+        const uint16_t* wa = w + static_cast<int64_t>(tile.a) * R * C + c0 + 4 * g;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int h = 0; h < NW / 4; ++h) {
+                uint2 rr[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 16 * s + 4 * q + i;
+                    rr[i] = (r < R && c0 + 32 * h + 4 * g < C)
+                                ? __ldg(reinterpret_cast<const uint2*>(wa + static_cast<int64_t>(r) * C + 32 * h))
+                                : make_uint2(0, 0);
+                }
+                b[s][4 * h][0] = __byte_perm(rr[0].x, rr[1].x, 0x5410);
+                b[s][4 * h][1] = __byte_perm(rr[2].x, rr[3].x, 0x5410);
+                b[s][4 * h + 1][0] = __byte_perm(rr[0].x, rr[1].x, 0x7632);
+                b[s][4 * h + 1][1] = __byte_perm(rr[2].x, rr[3].x, 0x7632);
+                b[s][4 * h + 2][0] = __byte_perm(rr[0].y, rr[1].y, 0x5410);
+                b[s][4 * h + 2][1] = __byte_perm(rr[2].y, rr[3].y, 0x5410);
+                b[s][4 * h + 3][0] = __byte_perm(rr[0].y, rr[1].y, 0x7632);
+                b[s][4 * h + 3][1] = __byte_perm(rr[2].y, rr[3].y, 0x7632);
+            }
+    }
+    __syncthreads();  // s_tok
+    // ring of base row segments: piece `lane % kPieces` of rows lane / kPieces + kRowsAt * i
+    uint8_t* const ring = dyn + BT * VP + warp * kExpandRing * 16 * P;
+    const uint32_t ring_s = sm100::smem_u32(ring);
+    const int pc = lane % kPieces, pr = lane / kPieces;
+    const int cp = c0 + 4 * pc;
+    auto fetch = [&](int i0) {
+        if (base && i0 < tile.count && cp < C) {
+            const uint32_t dst = ring_s + ((i0 >> 4) % kExpandRing) * 16 * P + pr * P + pc * 16;
+#pragma unroll
+            for (int i = 0; i < 16 / kRowsAt; ++i) {
+                const int tok = s_tok[i0 + pr + kRowsAt * i];
+                if (tok >= 0) cp_async16(dst + kRowsAt * i * P, base + tok * ld_base + cp, true);
+            }
+        }
+        cp_async_commit();
+    };
+    fetch(0);
+    fetch(16);
+    wait_previous();  // v
+    // v rows, four ranks at a time, zeros past the rank and the tile
+    {
+        const uint32_t v_s = sm100::smem_u32(dyn);
+        const float* vt = v + static_cast<int64_t>(tile.p0) * R;
+        for (int idx = threadIdx.x; idx < BT * KS * 4; idx += kExpandThreads) {
+            const int i = idx / (KS * 4), r = idx % (KS * 4) * 4;
+            const uint32_t dst = v_s + i * VP + r * 4;
+            if (R % 4 == 0) {
+                const bool in = i < tile.count && r < R;
+                cp_async16(dst, in ? vt + static_cast<int64_t>(i) * R + r : v, in);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const bool in = i < tile.count && r + u < R;
+                    cp_async4(dst + 4 * u, in ? vt + static_cast<int64_t>(i) * R + r + u : v, in);
+                }
+            }
+        }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
     __syncthreads();
     const float f = scales ? __ldg(scales + tile.a) : 1.0f;
-    const int cl = c0 + 2 * NW * q;  // the lane's 2 NW columns
     for (int i0 = 0; i0 < tile.count; i0 += 16) {
-        const int tok[2] = {s_tok[i0 + g], s_tok[i0 + 8 + g]};
-        float4 old[2][NW / 2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int u = 0; u < NW / 2; ++u)
-                old[h][u] = (base && tok[h] >= 0 && cl + 4 * u < C)
-                                ? *reinterpret_cast<const float4*>(base + tok[h] * ld_base + cl + 4 * u)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
+        fetch(i0 + 32);
         float acc[NW][4];
 #pragma unroll
         for (int j = 0; j < NW; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+        // rows g and g + 8, ranks 16 s + 4 q + 0..3: A operands of the terms h, m, l
+        uint32_t hi[KS][4], mid[KS][4];
+        const uint8_t* vr = dyn + (i0 + g) * VP + q * 16;
 #pragma unroll
-        for (int sp = 2; sp >= 0; --sp)  // the small terms first
+        for (int s = 0; s < KS; ++s) {
+            const float4 v0 = *reinterpret_cast<const float4*>(vr + s * 64);
+            const float4 v1 = *reinterpret_cast<const float4*>(vr + 8 * VP + s * 64);
+            uint32_t lo[4];
+            split3_pair(v0.x, v0.y, hi[s][0], mid[s][0], lo[0]);
+            split3_pair(v1.x, v1.y, hi[s][1], mid[s][1], lo[1]);
+            split3_pair(v0.z, v0.w, hi[s][2], mid[s][2], lo[2]);
+            split3_pair(v1.z, v1.w, hi[s][3], mid[s][3], lo[3]);
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const uint4 a = *reinterpret_cast<const uint4*>(&frag[i0 >> 4][sp][s][lane * 4]);
+            for (int j = 0; j < NW; ++j) mma_bf16(acc[j], lo[0], lo[1], lo[2], lo[3], b[s][j][0], b[s][j][1]);
+        }
+        // the small terms first
 #pragma unroll
-                for (int j = 0; j < NW; ++j) mma_bf16(acc[j], a.x, a.y, a.z, a.w, b[s][j][0], b[s][j][1]);
-            }
-        // acc[j][0], [1]: row g, columns cl + j and cl + NW + j; [2], [3]: row g + 8
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (tok[h] < 0) continue;
-            float o[2 * NW];
+            for (int j = 0; j < NW; ++j)
+                mma_bf16(acc[j], mid[s][0], mid[s][1], mid[s][2], mid[s][3], b[s][j][0], b[s][j][1]);
 #pragma unroll
-            for (int j = 0; j < NW; ++j) {
-                o[j] = acc[j][2 * h];
-                o[NW + j] = acc[j][2 * h + 1];
-            }
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int u = 0; u < NW / 2; ++u) {
-                if (cl + 4 * u >= C) continue;
-                const float4 r = make_float4(fmaf(f, o[4 * u], old[h][u].x), fmaf(f, o[4 * u + 1], old[h][u].y),
-                                             fmaf(f, o[4 * u + 2], old[h][u].z), fmaf(f, o[4 * u + 3], old[h][u].w));
-                *reinterpret_cast<float4*>(out + tok[h] * ld_out + cl + 4 * u) = r;
+            for (int j = 0; j < NW; ++j)
+                mma_bf16(acc[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], b[s][j][0], b[s][j][1]);
+        cp_async_wait<2>();
+        __syncwarp();
+        // acc[4 h + u][0], [1]: row g, columns 32 h + 8 q + u and + 4 + u; [2], [3]: row g + 8
+        uint8_t* const slot = ring + ((i0 >> 4) % kExpandRing) * 16 * P;
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr)
+#pragma unroll
+            for (int h = 0; h < NW / 4; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float4* at = reinterpret_cast<float4*>(slot + (g + 8 * hr) * P + (32 * h + 8 * q + 4 * e) * 4);
+                    const float4 o = base ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int n = 2 * hr + e;
+                    *at = make_float4(fmaf(f, acc[4 * h][n], o.x), fmaf(f, acc[4 * h + 1][n], o.y),
+                                      fmaf(f, acc[4 * h + 2][n], o.z), fmaf(f, acc[4 * h + 3][n], o.w));
+                }
+        __syncwarp();
+        if (cp < C) {
+#pragma unroll
+            for (int i = 0; i < 16 / kRowsAt; ++i) {
+                const int tok = s_tok[i0 + pr + kRowsAt * i];
+                if (tok < 0) continue;
+                const float4 r = *reinterpret_cast<const float4*>(slot + (pr + kRowsAt * i) * P + pc * 16);
+                *reinterpret_cast<float4*>(out + tok * ld_out + cp) = r;
                 if (out_bf16)
-                    *reinterpret_cast<uint2*>(out_bf16 + static_cast<int64_t>(tok[h]) * C + cl + 4 * u) =
+                    *reinterpret_cast<uint2*>(out_bf16 + static_cast<int64_t>(tok) * C + cp) =
                         make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
             }
         }
+        __syncwarp();  // the slot is free for the fetch of the next round
     }
 }
 
 // ------------------------------------------------------------------- outer
 //
-// d[a, r, c] = f_a sum_p v[p, r] x[tok, c].  A block holds 16 MR ranks times
-// 256 columns of one adapter in registers (a warp 64 columns) and walks over
-// the adapter's tokens.  Ranks are the rows of the MMA, tokens its K; two
-// token rows of x are interleaved into the B operand as in the expand.  Each
-// 16-token product of the three terms starts from zero and is added in FP32,
-// so no long sum is left to the tensor core's rounding.
+// d[a, r, c] = f_a sum_p v[p, r] x[tok, c], 64 ranks times 256 columns per
+// cluster on tcgen05; tokens are the K of the product, dealt in equal runs to
+// the cluster's blocks.  Both operands lie in shared memory token by token,
+// 64 values (128 bytes, 128-byte swizzle) per token and panel, so they are
+// MN-major: x comes in by cp.async (gathered rows), the three terms of v are
+// written by the threads, which split them on the way.  The three products
+// share the accumulator; it is moved to FP32 registers every kOuterChain
+// stages, so no long sum is left to the tensor core's rounding.  Two blocks
+// per SM cover each other's waits.  The blocks' sums are joined in block
+// order.
 constexpr int kOuterThreads = 128;
-constexpr int kOuterTokens = 64;
+constexpr int kOuterRanks = 64;
 constexpr int kOuterCols = 256;
+constexpr int kOuterTokens = 32;   // per stage
+constexpr int kOuterStages = 3;
+constexpr int kOuterChain = 8;
+constexpr int kOuterPanel = kOuterTokens * 128;
+constexpr int kOuterStageBytes = (kOuterCols / 64 + 3) * kOuterPanel;  // four panels of x, three of v
+constexpr int kOuterPitch = kOuterCols + 4;                            // floats per rank row of the block's sums
+constexpr int kOuterSmem = 1024 + kOuterStages * kOuterStageBytes;
+static_assert(kOuterRanks * kOuterPitch * 4 <= kOuterStages * kOuterStageBytes, "the sums reuse the ring");
 
-template <int MR>
+// Shared-memory matrix descriptor of an MN-major operand in the 128-byte
+// swizzle: panels of 64 MN values (128-byte rows, one per K index), 8 K rows
+// per 1024-byte atom (stride offset), panels `panel` bytes apart (leading
+// offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t panel)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(panel >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
 __global__ void __launch_bounds__(kOuterThreads)
     lora_outer_kernel(LoraRows rows, int R, int rblocks, LoraOuter pa, LoraOuter pb, int ablocks)
 {
-    __shared__ __align__(16) uint32_t frag[kOuterTokens / 16][3][MR][32 * 4];
-    __shared__ int s_tok[kOuterTokens];
-    const bool first = static_cast<int>(blockIdx.x) < ablocks;
-    const LoraOuter& pr = first ? pa : pb;
-    const int cblk = first ? blockIdx.x : blockIdx.x - ablocks;
+    constexpr int S = kOuterStages;
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(8) uint64_t s_bar[S];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int nc = static_cast<int>(cluster.num_blocks());
+    const int rank = static_cast<int>(cluster.block_rank());
+    const int blk = static_cast<int>(blockIdx.x) / nc;
+    const bool first = blk < ablocks;
+    const float* const pv = first ? pa.v : pb.v;
+    const uint16_t* const px = first ? pa.x : pb.x;
+    const int64_t ldx = first ? pa.ldx : pb.ldx;
+    const int C = first ? pa.C : pb.C;
+    const int c0 = (first ? blk : blk - ablocks) * kOuterCols;
     const int a = blockIdx.y / rblocks;
-    const int r0 = (blockIdx.y % rblocks) * 16 * MR;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, q = lane & 3;
+    const int r0 = (blockIdx.y % rblocks) * kOuterRanks;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    const uint32_t ring_s = sm100::smem_u32(ring);
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) sm100::mbar_init(sm100::smem_u32(&s_bar[i]), 1);
+        sm100::fence_barrier_init();
+        s_abort = 0;
+    }
+    if (warp == 0) {
+        sm100::tmem_alloc(sm100::smem_u32(&s_tmem), kOuterCols);
+        sm100::tmem_relinquish();
+    }
+    sm100::tc_fence_before();
+    __syncthreads();
+    sm100::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    // this block's run of the adapter's tokens, in whole stages
     const int T = static_cast<int>(rows.T);
-    const int p_lo = min(max(__ldg(rows.offsets + a), 0), T);
-    const int p_hi = min(max(__ldg(rows.offsets + a + 1), p_lo), T);
-    const int C = pr.C;
-    const int c0 = cblk * kOuterCols + warp * 64;
-    const int c = c0 + 8 * g;
-    float sum[MR][8][4];
+    const int lo = min(max(__ldg(rows.offsets + a), 0), T);
+    const int hi = min(max(__ldg(rows.offsets + a + 1), lo), T);
+    const int stages = (hi - lo + kOuterTokens - 1) / kOuterTokens;
+    const int s_lo = static_cast<int>(static_cast<int64_t>(stages) * rank / nc);
+    const int mine = static_cast<int>(static_cast<int64_t>(stages) * (rank + 1) / nc) - s_lo;
+    const int p0 = lo + s_lo * kOuterTokens;
+    // x: piece ch (8 columns) of panel j, token rows row0 and row0 + 16
+    const int ch = tid & 7, row0 = tid >> 3;
+    const uint32_t swz = static_cast<uint32_t>(ch ^ (row0 & 7)) << 4;
+    auto load_x = [&](int i) {
+        if (i < mine) {
+            const uint32_t dst = ring_s + (i % S) * kOuterStageBytes + row0 * 128 + swz;
 #pragma unroll
-    for (int m = 0; m < MR; ++m)
+            for (int h = 0; h < kOuterTokens / 16; ++h) {
+                const int p = p0 + i * kOuterTokens + row0 + 16 * h;
+                const int tok = p < hi ? __ldg(rows.tokens + p) : -1;
+                const bool row = tok >= 0 && tok < T;
+                const uint16_t* src = px + (row ? tok * ldx : 0) + c0 + ch * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[m][j][i] = 0.0f;
-    for (int p0 = p_lo; p0 < p_hi; p0 += kOuterTokens) {
-        const int count = min(kOuterTokens, p_hi - p0);
-        __syncthreads();
-        for (int i = threadIdx.x; i < kOuterTokens; i += kOuterThreads) {
-            const int tok = (i < count) ? __ldg(rows.tokens + p0 + i) : -1;
-            s_tok[i] = (tok >= 0 && tok < T) ? tok : -1;
-        }
-        for (int idx = threadIdx.x; idx < (kOuterTokens / 2) * MR * 16; idx += kOuterThreads) {
-            const int r = idx % (MR * 16), i = (idx / (MR * 16)) * 2;
-            Split t[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const bool in = i + u < count && r0 + r < R;
-                t[u] = split3(in ? __ldg(pr.v + static_cast<int64_t>(p0 + i + u) * R + r0 + r) : 0.0f);
-            }
-            // tokens 4 q + 2 h, + 1 of a group; ranks g and g + 8 of a 16-rank tile
-            const int at = ((((r & 7) * 4 + ((i & 15) >> 2)) << 2) | (((i >> 1) & 1) << 1) | ((r >> 3) & 1));
-            uint32_t* d = &frag[i >> 4][0][r >> 4][at];
-            d[0] = pack_bf16(t[0].h, t[1].h);
-            d[MR * 128] = pack_bf16(t[0].m, t[1].m);
-            d[2 * MR * 128] = pack_bf16(t[0].l, t[1].l);
-        }
-        __syncthreads();
-        for (int i0 = 0; i0 < count; i0 += 16) {
-            uint4 xr[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tok = s_tok[i0 + 4 * q + i];
-                xr[i] = (tok >= 0 && c < C) ? ldg16(pr.x + tok * pr.ldx + c) : make_uint4(0, 0, 0, 0);
-            }
-            uint32_t b[8][2];
-            const uint32_t(&w0)[4] = reinterpret_cast<const uint32_t(&)[4]>(xr[0]);
-            const uint32_t(&w1)[4] = reinterpret_cast<const uint32_t(&)[4]>(xr[1]);
-            const uint32_t(&w2)[4] = reinterpret_cast<const uint32_t(&)[4]>(xr[2]);
-            const uint32_t(&w3)[4] = reinterpret_cast<const uint32_t(&)[4]>(xr[3]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-                b[j][0] = __byte_perm(w0[j / 2], w1[j / 2], sel);
-                b[j][1] = __byte_perm(w2[j / 2], w3[j / 2], sel);
-            }
-#pragma unroll
-            for (int m = 0; m < MR; ++m) {
-                float t[8][4];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) t[j][i] = 0.0f;
-#pragma unroll
-                for (int sp = 2; sp >= 0; --sp) {
-                    const uint4 av = *reinterpret_cast<const uint4*>(&frag[i0 >> 4][sp][m][lane * 4]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) mma_bf16(t[j], av.x, av.y, av.z, av.w, b[j][0], b[j][1]);
+                for (int j = 0; j < kOuterCols / 64; ++j) {
+                    const bool ok = row && c0 + j * 64 + ch * 8 < C;
+                    cp_async16(dst + j * kOuterPanel + h * 2048, ok ? src + j * 64 : px, ok);
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[m][j][i] += t[j][i];
             }
+        }
+        cp_async_commit();
+    };
+    // v: token vt, ranks vr .. vr + 15 of the block's 64
+    const int vt = tid >> 2, vr = (tid & 3) * 16;
+    float va[16];
+    auto load_v = [&](int i) {
+        const int p = p0 + i * kOuterTokens + vt;
+        const bool row = i < mine && p < hi;
+        const float* src = pv + static_cast<int64_t>(p) * R + r0 + vr;
+        if (R % 4 == 0) {
+#pragma unroll
+            for (int u = 0; u < 16; u += 4) {
+                const float4 t = (row && r0 + vr + u < R) ? __ldcg(reinterpret_cast<const float4*>(src + u))
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                va[u] = t.x;
+                va[u + 1] = t.y;
+                va[u + 2] = t.z;
+                va[u + 3] = t.w;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 16; ++u) va[u] = (row && r0 + vr + u < R) ? __ldcg(src + u) : 0.0f;
+        }
+    };
+    auto store_v = [&](int i) {
+        uint8_t* const dst = ring + (i % S) * kOuterStageBytes + (kOuterCols / 64) * kOuterPanel + vt * 128;
+#pragma unroll
+        for (int u = 0; u < 16; u += 8) {
+            uint4 h, m, l;
+            split3_pair(va[u], va[u + 1], h.x, m.x, l.x);
+            split3_pair(va[u + 2], va[u + 3], h.y, m.y, l.y);
+            split3_pair(va[u + 4], va[u + 5], h.z, m.z, l.z);
+            split3_pair(va[u + 6], va[u + 7], h.w, m.w, l.w);
+            const int at = (((vr + u) >> 3) ^ (vt & 7)) << 4;
+            *reinterpret_cast<uint4*>(dst + at) = h;
+            *reinterpret_cast<uint4*>(dst + kOuterPanel + at) = m;
+            *reinterpret_cast<uint4*>(dst + 2 * kOuterPanel + at) = l;
+        }
+    };
+    float sum[kOuterCols / 64][32];
+#pragma unroll
+    for (int j = 0; j < kOuterCols / 64; ++j)
+#pragma unroll
+        for (int u = 0; u < 32; ++u) sum[j][u] = 0.0f;
+    bool alive = true;
+    auto wait_stage = [&](int i) {  // the MMAs of stage i are complete
+        alive = alive && sm100::mbar_wait_bounded(sm100::smem_u32(&s_bar[i % S]), (i / S) & 1,
+                                                  reinterpret_cast<volatile int*>(&s_abort), kTileWaitNs);
+    };
+    auto promote = [&]() {
+        sm100::tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < kOuterCols / 64; ++j) {
+            uint32_t t[32];
+            sm100::tmem_ld16x256_x8_issue(tmem + (static_cast<uint32_t>(warp) << 21) + j * 64, t);
+            sm100::tmem_ld_wait(t);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) sum[j][u] += __uint_as_float(t[u]);
+        }
+        sm100::tc_fence_before();
+    };
+    constexpr uint32_t idesc = idesc_bf16_f32(kOuterRanks, kOuterCols, 1, 1);
+    load_x(0);
+    load_x(1);
+    wait_previous();  // dv
+    load_v(0);
+    for (int i = 0; i < mine; ++i) {
+        store_v(i);
+        load_v(i + 1);
+        if (i > 0 && i % kOuterChain == 0) {
+            wait_stage(i - 1);
+            promote();
+        }
+        cp_async_wait<1>();
+        sm100::fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0 && alive) {
+            sm100::tc_fence_after();
+            const uint32_t st = ring_s + (i % S) * kOuterStageBytes;
+            const uint64_t dx = sw128_mnmajor_desc(st, kOuterPanel);
+            const uint64_t dv = sw128_mnmajor_desc(st + (kOuterCols / 64) * kOuterPanel, kOuterPanel);
+#pragma unroll
+            for (int kk = 0; kk < kOuterTokens / 16; ++kk)
+#pragma unroll
+                for (int sp = 2; sp >= 0; --sp)  // 16 token rows are 2048 bytes
+                    mma_f16_ss(tmem, dv + (sp * kOuterPanel + kk * 2048) / 16, dx + kk * 2048 / 16, idesc,
+                               (i % kOuterChain != 0 || kk != 0 || sp != 2) ? 1u : 0u);
+            sm100::mma_commit(sm100::smem_u32(&s_bar[i % S]));
+        }
+        if (i > 0) wait_stage(i - 1);
+        load_x(i + 2);
+    }
+    if (mine > 0) {
+        wait_stage(mine - 1);
+        promote();
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    if (warp == 0) {
+        sm100::tc_fence_after();
+        sm100::tmem_dealloc(tmem, kOuterCols);
+    }
+    // the block's sums: lane l holds ranks 16 warp + l / 4 (+ 8), columns
+    // 64 j + 8 i + 2 (l % 4) and + 1; a wait that ran out leaves NaN
+    float* const part = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int j = 0; j < kOuterCols / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float2 t = make_float2(sum[j][4 * i + 2 * h], sum[j][4 * i + 2 * h + 1]);
+                if (!alive) t = make_float2(NAN, NAN);
+                *reinterpret_cast<float2*>(part + (16 * warp + lane / 4 + 8 * h) * kOuterPitch + 64 * j + 8 * i +
+                                           2 * (lane % 4)) = t;
+            }
+    cluster.sync();
+    const float* const scales = first ? pa.scales : pb.scales;
+    const float f = scales ? __ldg(scales + a) : 1.0f;
+    float* const d = (first ? pa.d : pb.d) + static_cast<int64_t>(a) * R * C;
+    const int per = kOuterRanks / nc;  // this block's rank rows
+    for (int e = tid; e < per * (kOuterCols / 4); e += kOuterThreads) {
+        const int row = rank * per + e / (kOuterCols / 4), c = e % (kOuterCols / 4) * 4;
+        if (r0 + row >= R || c0 + c >= C) continue;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b = 0; b < nc; ++b) {
+            const float4 t = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, b) + row * kOuterPitch + c);
+            s.x += t.x;
+            s.y += t.y;
+            s.z += t.z;
+            s.w += t.w;
+        }
+        *reinterpret_cast<float4*>(d + static_cast<int64_t>(r0 + row) * C + c0 + c) =
+            make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
+    }
+    cluster.sync();  // the peers have read this block's sums
+}
+
+// A launch with up to two attributes: cluster size along x (0: none), and
+// programmatic launch after the kernel before it.
+struct Launch {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[2];
+    Launch(int64_t grid, int threads, size_t smem, cudaStream_t s, int cluster, bool programmatic)
+    {
+        cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cfg.attrs = at;
+        if (cluster) {
+            at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+            at[cfg.numAttrs].val.clusterDim.x = cluster;
+            at[cfg.numAttrs].val.clusterDim.y = 1;
+            at[cfg.numAttrs++].val.clusterDim.z = 1;
+        }
+        if (programmatic) {
+            at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
         }
     }
-    // sum[m][j][0], [1]: rank g, columns c0 + 16 q + j and + 8 + j; [2], [3]: rank g + 8
-    const float f = pr.scales ? __ldg(pr.scales + a) : 1.0f;
-#pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = r0 + m * 16 + g + 8 * h;
-            if (r >= R) continue;
-            float* d = pr.d + (static_cast<int64_t>(a) * R + r) * C;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int cc = c0 + 16 * q + 8 * half;
-                if (cc >= C) continue;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    *reinterpret_cast<float4*>(d + cc + 4 * u) =
-                        make_float4(f * sum[m][4 * u][2 * h + half], f * sum[m][4 * u + 1][2 * h + half],
-                                    f * sum[m][4 * u + 2][2 * h + half], f * sum[m][4 * u + 3][2 * h + half]);
-            }
-        }
+};
+
+// Dynamic shared memory beyond 48 KB is a per-device attribute of a kernel.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes)
+{
+    return bytes <= 48 * 1024 ? cudaSuccess
+                              : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     static_cast<int>(bytes));
+}
+
+// Blocks per cluster (they share the columns): enough to give every SM two
+// blocks, while each block keeps `least` column steps.
+int cluster_size(int64_t units, int steps, int least, int sm_count)
+{
+    int nc = 1;
+    while (nc < 8 && units * nc < 2 * sm_count && steps >= 2 * nc * least) nc *= 2;
+    return nc;
 }
 
 template <int MR>
@@ -474,22 +899,21 @@ cudaError_t shrink(const LoraRows& rows, const uint16_t* x, int64_t ldx, int C, 
 {
     const int rblocks = (R + 16 * MR - 1) / (16 * MR);
     const int64_t units = max_tiles(rows.T, rows.n, kShrinkTokens) * rblocks;
-    // as many blocks per cluster (they share the columns) as it takes to give
-    // every SM two blocks, while each warp keeps two column steps
-    int nc = 1;
-    while (nc < 8 && units * nc < 2 * sm_count && (C + 31) / 32 >= nc * 2 * (kShrinkThreads / 32) * 2) nc *= 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * nc));
-    cfg.blockDim = dim3(kShrinkThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = nc;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_shrink_kernel<MR>, rows, x, ldx, C, w, R, rblocks, scales, v);
+    const int nc = cluster_size(units, (C + 31) / 32, 2 * (kShrinkThreads / 32), sm_count);
+    Launch l(units * nc, kShrinkThreads, 0, s, nc, false);
+    return cudaLaunchKernelEx(&l.cfg, lora_shrink_kernel<MR>, rows, x, ldx, C, w, R, rblocks, scales, v);
+}
+
+template <int RP>
+cudaError_t shrink_tile(const LoraRows& rows, const uint16_t* x, int64_t ldx, int C, const uint16_t* w, int R,
+                        const float* scales, float* v, int sm_count, cudaStream_t s)
+{
+    const int64_t units = max_tiles(rows.T, rows.n, kTileTokens);
+    const int nc = cluster_size(units, (C + 63) / 64, 4, sm_count);
+    cudaError_t err = allow_smem(lora_shrink_tile_kernel<RP>, tile_smem(RP));
+    if (err != cudaSuccess) return err;
+    Launch l(units * nc, kTileThreads, tile_smem(RP), s, nc, false);
+    return cudaLaunchKernelEx(&l.cfg, lora_shrink_tile_kernel<RP>, rows, x, ldx, C, w, R, scales, v);
 }
 
 template <int KS, int NW, int BT>
@@ -498,20 +922,12 @@ cudaError_t expand(const LoraRows& rows, const float* v, int R, const uint16_t* 
 {
     const int cols = kExpandThreads / 32 * 8 * NW;
     const int cblocks = (C + cols - 1) / cols;
-    const int64_t grid = max_tiles(rows.T, rows.n, BT) * cblocks;
-    lora_expand_kernel<KS, NW, BT><<<static_cast<unsigned>(grid), kExpandThreads, 0, s>>>(
-        rows, v, R, w, C, cblocks, scales, base, ld_base, out, ld_out, out_bf16);
-    return cudaGetLastError();
-}
-
-template <int MR>
-cudaError_t outer(const LoraRows& rows, int R, const LoraOuter& a, const LoraOuter& b, cudaStream_t s)
-{
-    const int rblocks = (R + 16 * MR - 1) / (16 * MR);
-    const int ab = (a.C + kOuterCols - 1) / kOuterCols, bb = (b.C + kOuterCols - 1) / kOuterCols;
-    const dim3 grid(static_cast<unsigned>(ab + bb), static_cast<unsigned>(rows.n * rblocks));
-    lora_outer_kernel<MR><<<grid, kOuterThreads, 0, s>>>(rows, R, rblocks, a, b, ab);
-    return cudaGetLastError();
+    constexpr int smem = expand_smem<KS, NW, BT>();
+    cudaError_t err = allow_smem(lora_expand_kernel<KS, NW, BT>, smem);
+    if (err != cudaSuccess) return err;
+    Launch l(max_tiles(rows.T, rows.n, BT) * cblocks, kExpandThreads, smem, s, 0, true);
+    return cudaLaunchKernelEx(&l.cfg, lora_expand_kernel<KS, NW, BT>, rows, v, R, w, C, cblocks, scales, base, ld_base,
+                              out, ld_out, out_bf16);
 }
 
 }  // namespace
@@ -521,6 +937,12 @@ cudaError_t launch_lora_shrink(const LoraRows& rows, const uint16_t* x, int64_t 
 {
     DeviceInfo di;
     if (!device_info(&di)) return cudaErrorUnknown;
+    if (rows.T >= 256 && rows.T >= 16 * static_cast<int64_t>(rows.n)) {
+        if (R <= 16) return shrink_tile<16>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
+        if (R <= 32) return shrink_tile<32>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
+        if (R <= 64) return shrink_tile<64>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
+        return shrink_tile<128>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
+    }
     if (R <= 16) return shrink<1>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
     if (R <= 32) return shrink<2>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
     return shrink<4>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
@@ -538,9 +960,17 @@ cudaError_t launch_lora_expand(const LoraRows& rows, const float* v, int R, cons
 
 cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, const LoraOuter& b, cudaStream_t s)
 {
-    if (R <= 16) return outer<1>(rows, R, a, b, s);
-    if (R <= 32) return outer<2>(rows, R, a, b, s);
-    return outer<4>(rows, R, a, b, s);
+    const int rblocks = (R + kOuterRanks - 1) / kOuterRanks;
+    const int ab = (a.C + kOuterCols - 1) / kOuterCols, bb = (b.C + kOuterCols - 1) / kOuterCols;
+    // blocks per cluster (they share an adapter's tokens): about 128 tokens
+    // each, so that an adapter with many tokens does not outlast the others
+    int nc = 1;
+    while (nc < 8 && rows.T >= 2 * static_cast<int64_t>(nc) * rows.n * 128) nc *= 2;
+    cudaError_t err = allow_smem(lora_outer_kernel, kOuterSmem);
+    if (err != cudaSuccess) return err;
+    Launch l(static_cast<int64_t>(ab + bb) * nc, kOuterThreads, kOuterSmem, s, nc, true);
+    l.cfg.gridDim.y = static_cast<unsigned>(rows.n * rblocks);
+    return cudaLaunchKernelEx(&l.cfg, lora_outer_kernel, rows, R, rblocks, a, b, ab);
 }
 
 }  // namespace fp8moe
