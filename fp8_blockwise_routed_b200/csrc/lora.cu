@@ -66,20 +66,42 @@ __device__ __forceinline__ void split3_pair(float a, float b, uint32_t& h, uint3
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
 // 16 bytes from global to shared memory without registers; zeros if !in
-// (then nothing is read).
+// (then nothing is read).  No memory clobber: the waits that make the copies
+// visible have it, and with one here each copy's address would wait for the
+// copy before it (a stage of the tiled shrink took 0.55 us to issue so).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0));
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0));
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Arrives on the barrier once this thread's earlier cp.async are complete.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Column group of 16 FP32 accumulators of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
 // Programmatic launch: a kernel of a call lets the next one start its blocks
@@ -97,49 +119,75 @@ struct Tile {
     int count;
 };
 template <int THREADS>
+struct Tiles {
+    static constexpr int kPer = (1024 + THREADS - 1) / THREADS;  // n <= 1024
+    int lo[kPer], cnt[kPer];  // this thread's adapters
+    int64_t before;           // tiles of the adapters before them
+    int64_t total;            // all tiles
+    int per, bt;
+
+    __device__ __forceinline__ void scan(const LoraRows& rows, int bt_)
+    {
+        __shared__ int s_warp[THREADS / 32];
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int T = static_cast<int>(rows.T);
+        bt = bt_;
+        per = (rows.n + THREADS - 1) / THREADS;
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int a = threadIdx.x * per + i;
+            lo[i] = cnt[i] = 0;
+            if (i < per && a < rows.n) {
+                lo[i] = min(max(__ldg(rows.offsets + a), 0), T);
+                cnt[i] = min(max(__ldg(rows.offsets + a + 1), lo[i]), T) - lo[i];
+                mine += (cnt[i] + bt - 1) / bt;
+            }
+        }
+        int incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        before = incl - mine;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) before += s_warp[w];
+            total += s_warp[w];
+        }
+    }
+
+    // The whole block calls it; barriers before and after the result is set.
+    __device__ __forceinline__ Tile find(int64_t tile) const
+    {
+        __shared__ Tile s_tile;
+        if (threadIdx.x == 0) s_tile.a = -1;
+        __syncthreads();
+        int64_t first = before;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int nt = (cnt[i] + bt - 1) / bt;
+            if (tile >= first && tile < first + nt) {
+                const int skip = static_cast<int>(tile - first) * bt;
+                s_tile = Tile{static_cast<int>(threadIdx.x * per + i), lo[i] + skip, min(bt, cnt[i] - skip)};
+            }
+            first += nt;
+        }
+        __syncthreads();
+        return s_tile;
+    }
+};
+
+template <int THREADS>
 __device__ __forceinline__ Tile find_tile(const LoraRows& rows, int bt, int64_t tile)
 {
-    __shared__ int s_warp[THREADS / 32];
-    __shared__ Tile s_tile;
-    const int lane = threadIdx.x & 31;
-    const int warp = threadIdx.x >> 5;
-    const int T = static_cast<int>(rows.T);
-    constexpr int kMaxPer = 1024 / THREADS;  // n <= 1024
-    if (threadIdx.x == 0) s_tile.a = -1;
-    int lo[kMaxPer], cnt[kMaxPer];
-    int mine = 0;
-    const int per = (rows.n + THREADS - 1) / THREADS;
-#pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) {
-        const int a = threadIdx.x * per + i;
-        lo[i] = cnt[i] = 0;
-        if (i < per && a < rows.n) {
-            lo[i] = min(max(__ldg(rows.offsets + a), 0), T);
-            cnt[i] = min(max(__ldg(rows.offsets + a + 1), lo[i]), T) - lo[i];
-            mine += (cnt[i] + bt - 1) / bt;
-        }
-    }
-    int incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-        if (lane >= off) incl += o;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - mine;
-    for (int w = 0; w < warp; ++w) before += s_warp[w];
-#pragma unroll
-    for (int i = 0; i < kMaxPer; ++i) {
-        const int nt = (cnt[i] + bt - 1) / bt;
-        if (tile >= before && tile < before + nt) {
-            const int skip = static_cast<int>(tile - before) * bt;
-            s_tile = Tile{static_cast<int>(threadIdx.x * per + i), lo[i] + skip, min(bt, cnt[i] - skip)};
-        }
-        before += nt;
-    }
-    __syncthreads();
-    return s_tile;
+    Tiles<THREADS> t;
+    t.scan(rows, bt);
+    return t.find(tile);
 }
 
 // Tiles of bt tokens that T tokens over n adapters can need at most.
@@ -250,22 +298,26 @@ __global__ void __launch_bounds__(kShrinkThreads)
 // The same product for adapters with many tokens: 128 tokens times all ranks
 // per cluster on tcgen05, the columns dealt to the cluster's blocks 64 at a
 // time.  A stage holds the 128 token rows and the RP rank rows of 64 columns
-// (128-byte rows, 128-byte swizzle, filled by cp.async, which gathers the
-// token rows and zero-fills what is missing); one thread issues the four MMAs
-// of a stage.  The accumulator is moved from TMEM to FP32 registers every
-// four stages (two TMEM buffers in turn), so a chain on the tensor core stays
-// 256 columns long.  At the end the blocks' sums are joined in block order.
+// (128-byte rows, 128-byte swizzle); four producer warps bring in the token
+// rows by cp.async, which gathers them and zero-fills what is missing, one TMA
+// box the rank rows (cp.async sustains about 40 bytes per clock and SM, which
+// these rows would share), and one thread issues the four MMAs.  Four more warps move the accumulator to FP32
+// registers every four stages (two TMEM buffers in turn), so a chain on the
+// tensor core stays 256 columns long (unbroken, 16384 columns come out 2e-6
+// off; so, 2.4e-7).  The producers neither fence nor read TMEM: both wait for
+// a thread's copies in flight, which kept one stage in flight instead of S
+// (16384 x 6144, rank 64: 72 us against %SHRINK%).  The proxy fence is the
+// issuer's, behind the barrier that the copies arrive on.  At the end the
+// blocks' sums are joined in block order.
 constexpr int kTileTokens = 128;
-constexpr int kTileThreads = 128;
-constexpr int kTileChain = 4;  // stages per accumulation chain
+constexpr int kTileThreads = 288;  // four warps of sums, four producers, the issuer
+constexpr int kTileChain = 4;      // stages per accumulation chain
 constexpr uint64_t kTileWaitNs = 2000000000ull;
 
-constexpr int tile_stages(int RP) { return RP <= 64 ? 4 : 3; }
+constexpr int tile_stages(int RP) { return RP <= 64 ? 4 : 6; }
+constexpr int tile_blocks(int RP) { return RP <= 64 ? 2 : 1; }  // per SM
 constexpr int tile_stage_bytes(int RP) { return (kTileTokens + RP) * 128; }
-constexpr int tile_smem(int RP)
-{
-    return 1024 + tile_stages(RP) * tile_stage_bytes(RP);
-}
+constexpr int tile_smem(int RP) { return 1024 + tile_stages(RP) * tile_stage_bytes(RP); }
 constexpr uint32_t tile_acc(int RP) { return RP <= 32 ? 32 : RP; }  // TMEM columns of one accumulator
 constexpr uint32_t tile_tmem(int RP) { return 2 * tile_acc(RP); }
 
@@ -289,17 +341,37 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, in
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Shared-memory matrix descriptor of an MN-major operand in the 128-byte
+// swizzle: panels of 64 MN values (128-byte rows, one per K index), 8 K rows
+// per 1024-byte atom (stride offset), panels `panel` bytes apart (leading
+// offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t panel)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(panel >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// K-major operand of 128 token rows in panels of 64 columns: its descriptor
+// from column `col` on (a multiple of 16).
+__device__ __forceinline__ uint64_t sw128_kmajor_desc_at(uint32_t smem_addr, int col)
+{
+    return sm100::sw128_kmajor_desc(smem_addr + (col >> 6) * kTileTokens * 128) + (col & 63) * 2 / 16;
+}
+
 template <int RP>
-__global__ void __launch_bounds__(kTileThreads)
-    lora_shrink_tile_kernel(LoraRows rows, const uint16_t* __restrict__ x, int64_t ldx, int C,
-                            const uint16_t* __restrict__ w, int R, const float* __restrict__ scales,
-                            float* __restrict__ v)
+__global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
+    lora_shrink_tile_kernel(const __grid_constant__ CUtensorMap wmap, LoraRows rows, const uint16_t* __restrict__ x,
+                            int64_t ldx, int C, int R, const float* __restrict__ scales, float* __restrict__ v)
 {
     constexpr int S = tile_stages(RP);
     constexpr int kStage = tile_stage_bytes(RP);
-    constexpr int RL = (RP + 31) / 32 * 32;  // accumulator columns read
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t s_bar[S];
+    __shared__ __align__(8) uint64_t s_full[S], s_empty[S], s_ready[2], s_read[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ int s_tok[kTileTokens];
@@ -311,113 +383,155 @@ __global__ void __launch_bounds__(kTileThreads)
     if (tile.a < 0) return;  // the whole cluster
     uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
     const uint32_t ring_s = sm100::smem_u32(ring);
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) sm100::mbar_init(sm100::smem_u32(&s_bar[i]), 1);
+        for (int i = 0; i < S; ++i) {
+            sm100::mbar_init(sm100::smem_u32(&s_full[i]), 128 + 1);  // the copies of x, the box of w
+            sm100::mbar_init(sm100::smem_u32(&s_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            sm100::mbar_init(sm100::smem_u32(&s_ready[i]), 1);
+            sm100::mbar_init(sm100::smem_u32(&s_read[i]), 128);
+        }
         sm100::fence_barrier_init();
         s_abort = 0;
     }
-    if (warp == 0) {
+    if (warp == 8) {
         sm100::tmem_alloc(sm100::smem_u32(&s_tmem), tile_tmem(RP));
         sm100::tmem_relinquish();
     }
-    {
-        int tok = (tid < tile.count) ? __ldg(rows.tokens + tile.p0 + tid) : -1;
+    if (tid < kTileTokens) {
+        const int tok = (tid < tile.count) ? __ldg(rows.tokens + tile.p0 + tid) : -1;
         s_tok[tid] = (tok >= 0 && tok < rows.T) ? tok : -1;
     }
     sm100::tc_fence_before();
     __syncthreads();
     sm100::tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const uint16_t* wa = w + static_cast<int64_t>(tile.a) * R * C;
-    const int ch = tid & 7, row0 = tid >> 3;
     const int chunks = (C + 63) / 64;
     const int mine = (chunks - rank + nc - 1) / nc;  // this block's: rank, rank + nc, ...
-    const uint32_t swz = (static_cast<uint32_t>(ch ^ (row0 & 7)) << 4);
-    auto load = [&](int i) {
-        if (i < mine) {
+    auto wait = [&](uint64_t* b, int phase) {
+        return sm100::mbar_wait_bounded(sm100::smem_u32(b), phase & 1, &s_abort, kTileWaitNs);
+    };
+    constexpr int kPitch = RP + 4;
+    float* const part = reinterpret_cast<float*>(ring);
+    float sum[RP];
+    if (warp < 4) {
+#pragma unroll
+        for (int r = 0; r < RP; ++r) sum[r] = 0.0f;
+        const int chains = (mine + kTileChain - 1) / kTileChain;
+        for (int c = 0; c < chains; ++c) {
+            if (!wait(&s_ready[c & 1], c >> 1)) break;
+            __syncwarp();
+            sm100::tc_fence_after();
+#pragma unroll
+            for (int c0 = 0; c0 < RP; c0 += 16) {
+                uint32_t t[16];
+                tmem_ld16(tmem + (static_cast<uint32_t>(warp) << 21) + (c & 1) * tile_acc(RP) + c0, t);
+#pragma unroll
+                for (int u = 0; u < 16; ++u) sum[c0 + u] += __uint_as_float(t[u]);
+            }
+            sm100::tc_fence_before();
+            sm100::mbar_arrive(sm100::smem_u32(&s_read[c & 1]));
+        }
+    } else if (warp < 8) {
+        const int ch = tid & 7, row0 = (tid >> 3) & 15;
+        const uint32_t swz = static_cast<uint32_t>(ch ^ (row0 & 7)) << 4;
+        const uint16_t* xr[kTileTokens / 16];
+        uint32_t have = 0;
+#pragma unroll
+        for (int j = 0; j < kTileTokens / 16; ++j) {
+            const int tok = s_tok[row0 + 16 * j];
+            xr[j] = x + (tok >= 0 ? tok * ldx : 0);
+            have |= (tok >= 0 ? 1u : 0u) << j;
+        }
+        for (int i = 0; i < mine; ++i) {
+            if (i >= S && !wait(&s_empty[i % S], i / S - 1)) break;
             const int k = (rank + i * nc) * 64 + ch * 8;
             const bool in = k < C;
+            const int kc = in ? k : 0;
             const uint32_t dst = ring_s + (i % S) * kStage + row0 * 128 + swz;
 #pragma unroll
-            for (int j = 0; j < kTileTokens / 16; ++j) {
-                const int tok = s_tok[row0 + 16 * j];
-                const bool ok = in && tok >= 0;
-                cp_async16(dst + j * 2048, ok ? x + tok * ldx + k : x, ok);
-            }
-#pragma unroll
-            for (int j = 0; j < RP / 16; ++j) {
-                const int r = row0 + 16 * j;
-                const bool ok = in && r < R;
-                cp_async16(dst + kTileTokens * 128 + j * 2048, ok ? wa + static_cast<int64_t>(r) * C + k : w, ok);
+            for (int j = 0; j < kTileTokens / 16; ++j) cp_async16(dst + j * 2048, xr[j] + kc, in && ((have >> j) & 1u));
+            cp_async_arrive(sm100::smem_u32(&s_full[i % S]));
+            if (tid == 128) {  // rank rows past R come in as zeros
+                const uint32_t bar = sm100::smem_u32(&s_full[i % S]);
+                sm100::mbar_arrive_expect_tx(bar, RP * 128);
+                sm100::tma_load_3d(ring_s + (i % S) * kStage + kTileTokens * 128, &wmap, (rank + i * nc) * 128, 0,
+                                   tile.a, bar);
             }
         }
-        cp_async_commit();
-    };
-    float sum[RL];
-#pragma unroll
-    for (int r = 0; r < RL; ++r) sum[r] = 0.0f;
-    bool alive = true;
-    auto wait_stage = [&](int i) {  // the MMAs of this block's i-th step are complete
-        alive = alive && sm100::mbar_wait_bounded(sm100::smem_u32(&s_bar[i % S]), (i / S) & 1,
-                                                  reinterpret_cast<volatile int*>(&s_abort), kTileWaitNs);
-    };
-    auto promote = [&](int chain) {
-        sm100::tc_fence_after();
-#pragma unroll
-        for (int c0 = 0; c0 < RL; c0 += 32) {
-            uint32_t t[32];
-            sm100::tmem_ld32_issue(tmem + (static_cast<uint32_t>(warp) << 21) + (chain & 1) * tile_acc(RP) + c0, t);
-            sm100::tmem_ld_wait(t);
-#pragma unroll
-            for (int u = 0; u < 32; ++u) sum[c0 + u] += __uint_as_float(t[u]);
+        cp_async_wait_all();
+    } else {
+        constexpr uint32_t idesc = idesc_bf16_f32(kTileTokens, RP, 0, 0);
+        // one thread runs the whole loop: votes and per-step index arithmetic
+        // would pace a stage's four MMAs
+        if (lane == 0) {
+            const uint64_t da0 = sm100::sw128_kmajor_desc(ring_s);
+            const uint64_t db0 = sm100::sw128_kmajor_desc(ring_s + kTileTokens * 128);
+            int st = 0, turn = 0, step = 0, c = 0;
+            for (int i = 0; i < mine; ++i) {
+                if (step == 0 && c >= 2 && !wait(&s_read[c & 1], (c >> 1) - 1)) break;
+                if (!wait(&s_full[st], turn)) break;
+                sm100::fence_proxy_async_smem();
+                sm100::tc_fence_after();
+                const uint64_t da = da0 + st * (kStage / 16), db = db0 + st * (kStage / 16);
+                const uint32_t d = tmem + (c & 1) * tile_acc(RP);
+                mma_f16_ss(d, da, db, idesc, step != 0 ? 1u : 0u);
+                mma_f16_ss(d, da + 2, db + 2, idesc, 1u);
+                mma_f16_ss(d, da + 4, db + 4, idesc, 1u);
+                mma_f16_ss(d, da + 6, db + 6, idesc, 1u);
+                sm100::mma_commit(sm100::smem_u32(&s_empty[st]));
+                if (++step == kTileChain || i == mine - 1) {
+                    sm100::mma_commit(sm100::smem_u32(&s_ready[c & 1]));
+                    step = 0;
+                    ++c;
+                }
+                if (++st == S) {
+                    st = 0;
+                    ++turn;
+                }
+            }
         }
-        sm100::tc_fence_before();
-    };
-    for (int i = 0; i < S - 1; ++i) load(i);
-    constexpr uint32_t idesc = idesc_bf16_f32(kTileTokens, RP, 0, 0);
-    for (int i = 0; i < mine; ++i) {
-        cp_async_wait<S - 2>();
-        sm100::fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0 && alive) {
-            sm100::tc_fence_after();
-            const uint32_t st = ring_s + (i % S) * kStage;
-            const uint64_t da = sm100::sw128_kmajor_desc(st), db = sm100::sw128_kmajor_desc(st + kTileTokens * 128);
-            const uint32_t d = tmem + ((i / kTileChain) & 1) * tile_acc(RP);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_f16_ss(d, da + 2 * kk, db + 2 * kk, idesc, (i % kTileChain != 0 || kk != 0) ? 1u : 0u);
-            sm100::mma_commit(sm100::smem_u32(&s_bar[i % S]));
-        }
-        if (i > 0) {
-            wait_stage(i - 1);
-            if (i % kTileChain == 0) promote(i / kTileChain - 1);
-        }
-        load(i + S - 1);
+        __syncwarp();
     }
-    wait_stage(mine - 1);
-    promote((mine - 1) / kTileChain);
-    cp_async_wait<0>();
-    __syncthreads();
-    if (warp == 0) {
+    __syncthreads();  // every chain is read: the MMAs and the ring are done with
+    if (warp == 8) {
         sm100::tc_fence_after();
         sm100::tmem_dealloc(tmem, tile_tmem(RP));
     }
     // the block's sums, rank-minor; a wait that ran out leaves NaN
-    constexpr int kPitch = RP + 1;
-    float* const part = reinterpret_cast<float*>(ring);
+    if (warp < 4) {
+        const bool bad = s_abort != 0;
 #pragma unroll
-    for (int r = 0; r < RP; ++r) part[tid * kPitch + r] = alive ? sum[r] : NAN;
+        for (int r = 0; r < RP; r += 4)
+            *reinterpret_cast<float4*>(part + tid * kPitch + r) =
+                bad ? make_float4(NAN, NAN, NAN, NAN) : make_float4(sum[r], sum[r + 1], sum[r + 2], sum[r + 3]);
+    }
     cluster.sync();
     const float f = scales ? __ldg(scales + tile.a) : 1.0f;
     const int per = kTileTokens / nc;  // this block's token rows
-    for (int e = tid; e < per * RP; e += kTileThreads) {
-        const int row = rank * per + e / RP, r = e % RP;
+#pragma unroll 4
+    for (int e = tid; e < per * (RP / 4); e += kTileThreads) {
+        const int row = rank * per + e / (RP / 4), r = e % (RP / 4) * 4;
         if (row >= tile.count || r >= R) continue;
-        float s = 0.0f;
-        for (int b = 0; b < nc; ++b) s += cluster.map_shared_rank(part, b)[row * kPitch + r];
-        v[static_cast<int64_t>(tile.p0 + row) * R + r] = f * s;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b = 0; b < nc; ++b) {
+            const float4 t = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, b) + row * kPitch + r);
+            s.x += t.x;
+            s.y += t.y;
+            s.z += t.z;
+            s.w += t.w;
+        }
+        float* const d = v + static_cast<int64_t>(tile.p0 + row) * R + r;
+        if (R % 4 == 0) {
+            *reinterpret_cast<float4*>(d) = make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
+        } else {
+            d[0] = f * s.x;
+            if (r + 1 < R) d[1] = f * s.y;
+            if (r + 2 < R) d[2] = f * s.z;
+            if (r + 3 < R) d[3] = f * s.w;
+        }
     }
     cluster.sync();  // the peers have read this block's sums
 }
@@ -431,29 +545,22 @@ __global__ void __launch_bounds__(kTileThreads)
 // 32 (j / 4) + 4 g + j % 4, so that a lane ends up with 8 consecutive columns
 // per row.  The base rows of the next two groups are on their way to a
 // per-warp ring in shared memory meanwhile; the sum is formed there in place
-// and written out in whole row segments.  v waits in shared memory in FP32 and
-// is split as it is read (each warp for itself: the splits hide under the
-// MMAs, where preparing them once per block stood in front of them).
+// and written out in whole row segments.  The split
+// terms of v wait in shared memory in the order of the A operand.
 constexpr int kExpandThreads = 128;
-constexpr int kExpandRing = 3;
 
 template <int NW>
 constexpr int expand_pitch()  // bytes of a ring row: 16 past a multiple of 128, so fragment reads do not collide
 {
     return 32 * NW + 16;
 }
-template <int KS>
-constexpr int expand_v_pitch()  // bytes of a row of v: 64 past a multiple of 128, as two rows are read at once
-{
-    return KS == 1 ? 64 : 64 * KS + 64;
-}
-template <int KS, int NW, int BT>
+template <int KS, int NW, int BT, int RING>
 constexpr int expand_smem()
 {
-    return BT * expand_v_pitch<KS>() + (kExpandThreads / 32) * kExpandRing * 16 * expand_pitch<NW>();
+    return (BT / 16) * 3 * KS * 512 + (kExpandThreads / 32) * RING * 16 * expand_pitch<NW>();
 }
 
-template <int KS, int NW, int BT>
+template <int KS, int NW, int BT, int RING>
 __global__ void __launch_bounds__(kExpandThreads)
     lora_expand_kernel(LoraRows rows, const float* v, int R, const uint16_t* __restrict__ w, int C, int cblocks,
                        const float* __restrict__ scales, const float* base, int64_t ld_base, float* out,
@@ -463,14 +570,17 @@ __global__ void __launch_bounds__(kExpandThreads)
     constexpr int kPieces = 2 * NW;         // 16-byte pieces of a row segment
     constexpr int kRowsAt = 32 / kPieces;   // rows a warp moves per instruction
     extern __shared__ __align__(16) uint8_t dyn[];
-    constexpr int VP = expand_v_pitch<KS>();
+    uint32_t* const frag = reinterpret_cast<uint32_t*>(dyn);  // [BT / 16][3][KS][32 * 4]
     __shared__ int s_tok[BT];
     allow_next();
     const Tile tile = find_tile<kExpandThreads>(rows, BT, blockIdx.x / cblocks);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, q = lane & 3;
     const int c0 = (static_cast<int>(blockIdx.x % cblocks) * (kExpandThreads / 32) + warp) * 8 * NW;
-    if (tile.a < 0) return;
+    if (tile.a < 0) {
+        wait_previous();  // so that this kernel never ends before the one it follows
+        return;
+    }
     for (int i = threadIdx.x; i < BT; i += kExpandThreads) {
         const int tok = (i < tile.count) ? __ldg(rows.tokens + tile.p0 + i) : -1;
         s_tok[i] = (tok >= 0 && tok < rows.T) ? tok : -1;
@@ -503,13 +613,13 @@ __global__ void __launch_bounds__(kExpandThreads)
     }
     __syncthreads();  // s_tok
     // ring of base row segments: piece `lane % kPieces` of rows lane / kPieces + kRowsAt * i
-    uint8_t* const ring = dyn + BT * VP + warp * kExpandRing * 16 * P;
+    uint8_t* const ring = dyn + (BT / 16) * 3 * KS * 512 + warp * RING * 16 * P;
     const uint32_t ring_s = sm100::smem_u32(ring);
     const int pc = lane % kPieces, pr = lane / kPieces;
     const int cp = c0 + 4 * pc;
     auto fetch = [&](int i0) {
         if (base && i0 < tile.count && cp < C) {
-            const uint32_t dst = ring_s + ((i0 >> 4) % kExpandRing) * 16 * P + pr * P + pc * 16;
+            const uint32_t dst = ring_s + ((i0 >> 4) % RING) * 16 * P + pr * P + pc * 16;
 #pragma unroll
             for (int i = 0; i < 16 / kRowsAt; ++i) {
                 const int tok = s_tok[i0 + pr + kRowsAt * i];
@@ -518,69 +628,69 @@ __global__ void __launch_bounds__(kExpandThreads)
         }
         cp_async_commit();
     };
-    fetch(0);
-    fetch(16);
+#pragma unroll
+    for (int i = 0; i < RING - 1; ++i) fetch(16 * i);
     wait_previous();  // v
-    // v rows, four ranks at a time, zeros past the rank and the tile
+    // the terms of v, four ranks of one token at a time, in the order of the A
+    // operand: lane 4 g + q holds rows g, g + 8 and ranks 16 s + 4 q + 0..3
     {
-        const uint32_t v_s = sm100::smem_u32(dyn);
+        constexpr int kEach = BT * KS * 4 / kExpandThreads;
+        float t[kEach][4];  // all loads before the first use
         const float* vt = v + static_cast<int64_t>(tile.p0) * R;
-        for (int idx = threadIdx.x; idx < BT * KS * 4; idx += kExpandThreads) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int idx = threadIdx.x + e * kExpandThreads;
             const int i = idx / (KS * 4), r = idx % (KS * 4) * 4;
-            const uint32_t dst = v_s + i * VP + r * 4;
             if (R % 4 == 0) {
-                const bool in = i < tile.count && r < R;
-                cp_async16(dst, in ? vt + static_cast<int64_t>(i) * R + r : v, in);
+                const float4 u = (i < tile.count && r < R)
+                                     ? __ldcg(reinterpret_cast<const float4*>(vt + static_cast<int64_t>(i) * R + r))
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                t[e][0] = u.x;
+                t[e][1] = u.y;
+                t[e][2] = u.z;
+                t[e][3] = u.w;
             } else {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const bool in = i < tile.count && r + u < R;
-                    cp_async4(dst + 4 * u, in ? vt + static_cast<int64_t>(i) * R + r + u : v, in);
-                }
+                for (int u = 0; u < 4; ++u)
+                    t[e][u] = (i < tile.count && r + u < R) ? __ldcg(vt + static_cast<int64_t>(i) * R + r + u) : 0.0f;
             }
         }
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int idx = threadIdx.x + e * kExpandThreads;
+            const int i = idx / (KS * 4), r4 = idx % (KS * 4);
+            uint2 h, m, l;
+            split3_pair(t[e][0], t[e][1], h.x, m.x, l.x);
+            split3_pair(t[e][2], t[e][3], h.y, m.y, l.y);
+            uint32_t* d = frag + ((i >> 4) * 3 * KS + (r4 >> 2)) * 128 + ((i & 7) * 4 + (r4 & 3)) * 4 +
+                          ((i >> 3) & 1) * 2;
+            *reinterpret_cast<uint2*>(d) = h;
+            *reinterpret_cast<uint2*>(d + KS * 128) = m;
+            *reinterpret_cast<uint2*>(d + 2 * KS * 128) = l;
+        }
     }
-    cp_async_commit();
-    cp_async_wait<0>();
     __syncthreads();
     const float f = scales ? __ldg(scales + tile.a) : 1.0f;
     for (int i0 = 0; i0 < tile.count; i0 += 16) {
-        fetch(i0 + 32);
+        fetch(i0 + 16 * (RING - 1));
         float acc[NW][4];
 #pragma unroll
         for (int j = 0; j < NW; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-        // rows g and g + 8, ranks 16 s + 4 q + 0..3: A operands of the terms h, m, l
-        uint32_t hi[KS][4], mid[KS][4];
-        const uint8_t* vr = dyn + (i0 + g) * VP + q * 16;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const float4 v0 = *reinterpret_cast<const float4*>(vr + s * 64);
-            const float4 v1 = *reinterpret_cast<const float4*>(vr + 8 * VP + s * 64);
-            uint32_t lo[4];
-            split3_pair(v0.x, v0.y, hi[s][0], mid[s][0], lo[0]);
-            split3_pair(v1.x, v1.y, hi[s][1], mid[s][1], lo[1]);
-            split3_pair(v0.z, v0.w, hi[s][2], mid[s][2], lo[2]);
-            split3_pair(v1.z, v1.w, hi[s][3], mid[s][3], lo[3]);
+        for (int sp = 2; sp >= 0; --sp)  // the small terms first
 #pragma unroll
-            for (int j = 0; j < NW; ++j) mma_bf16(acc[j], lo[0], lo[1], lo[2], lo[3], b[s][j][0], b[s][j][1]);
-        }
-        // the small terms first
+            for (int s = 0; s < KS; ++s) {
+                const uint4 a =
+                    *reinterpret_cast<const uint4*>(frag + (((i0 >> 4) * 3 + sp) * KS + s) * 128 + lane * 4);
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int j = 0; j < NW; ++j)
-                mma_bf16(acc[j], mid[s][0], mid[s][1], mid[s][2], mid[s][3], b[s][j][0], b[s][j][1]);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int j = 0; j < NW; ++j)
-                mma_bf16(acc[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], b[s][j][0], b[s][j][1]);
-        cp_async_wait<2>();
+                for (int j = 0; j < NW; ++j) mma_bf16(acc[j], a.x, a.z, a.y, a.w, b[s][j][0], b[s][j][1]);
+            }
+        cp_async_wait<RING - 1>();
         __syncwarp();
         // acc[4 h + u][0], [1]: row g, columns 32 h + 8 q + u and + 4 + u; [2], [3]: row g + 8
-        uint8_t* const slot = ring + ((i0 >> 4) % kExpandRing) * 16 * P;
+        uint8_t* const slot = ring + ((i0 >> 4) % RING) * 16 * P;
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr)
 #pragma unroll
@@ -610,51 +720,311 @@ __global__ void __launch_bounds__(kExpandThreads)
     }
 }
 
+// The same product for adapters with many tokens, on tcgen05: 128 tokens times
+// W columns at a time, one persistent block per SM over an equal run of
+// (tile, column block) items.  The split terms of a tile's v rows lie in
+// shared memory as one K-major operand [h | m | l] (3 RP wide) and stay for
+// all its columns; the adapter's rank rows of W columns are the other,
+// MN-major, by TMA, used once per term.  Base rows come in by cp.async; a
+// thread of the epilogue owns one row (TMEM lane), forms its sums in place, and
+// its warp writes the rows out whole.  (One bulk copy per row and direction
+// instead: 206 us against 172 us for 16384 x 6144, rank 64; the copy engine
+// takes a request about every 32 clocks, whatever its size.)  Two
+// row buffers, each with its own four epilogue warps, take turns; the products
+// run up to four blocks ahead of them (four accumulators in TMEM, two slabs),
+// so a buffer only waits for its base rows.
+constexpr int kWideThreads = 416;  // two epilogue groups of 128, the issuer's warp, four producer warps
+constexpr int wide_cols(int RP) { return RP <= 64 ? 128 : 64; }
+constexpr int wide_panels(int RP) { return (3 * RP + 63) / 64; }
+constexpr int wide_pitch(int RP) { return wide_cols(RP) * 4 + 16; }  // bytes of a base row, off the bank period
+constexpr int wide_slab(int RP) { return RP * wide_cols(RP) * 2; }
+constexpr int wide_smem(int RP)
+{
+    return 1024 + wide_panels(RP) * kTileTokens * 128 + 2 * (wide_slab(RP) + kTileTokens * wide_pitch(RP));
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    lora_expand_tile_kernel(const __grid_constant__ CUtensorMap wmap, LoraRows rows, const float* v, int R, int C,
+                            const float* __restrict__ scales, const float* base, int64_t ld_base, float* out,
+                            int64_t ld_out, uint16_t* __restrict__ out_bf16)
+{
+    constexpr int W = wide_cols(RP);
+    constexpr int NP = wide_panels(RP);
+    constexpr int P = wide_pitch(RP);
+    constexpr uint32_t kSlab = wide_slab(RP);
+    extern __shared__ uint8_t dyn[];
+    // barriers: base rows in and buffer free (2 buffers), slab in and used
+    // (2 slabs), sums ready and read (4 accumulators)
+    __shared__ __align__(8) uint64_t s_bar[16];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ int s_tok[kTileTokens];
+    uint8_t* const mem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    uint8_t* const slabs = mem + NP * kTileTokens * 128;
+    uint8_t* const bufs = slabs + 2 * kSlab;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    volatile int* const abort = &s_abort;
+    enum { kBaseIn = 0, kFree = 2, kSlabIn = 4, kSlabUsed = 6, kReady = 8, kRead = 12 };
+    auto bar = [&](int kind, int i) { return sm100::smem_u32(&s_bar[kind + i]); };
+    auto wait = [&](uint32_t b, uint32_t phase) {
+        return sm100::mbar_wait_bounded(b, phase & 1, abort, kTileWaitNs);
+    };
+    allow_next();
+    if (tid == 0) {
+        for (int b = 0; b < 2; ++b) {
+            sm100::mbar_init(bar(kBaseIn, b), 128);
+            sm100::mbar_init(bar(kFree, b), 128);
+            sm100::mbar_init(bar(kSlabIn, b), 1);
+            sm100::mbar_init(bar(kSlabUsed, b), 1);
+        }
+        for (int d = 0; d < 4; ++d) {
+            sm100::mbar_init(bar(kReady, d), 1);
+            sm100::mbar_init(bar(kRead, d), 128);
+        }
+        sm100::fence_barrier_init();
+        s_abort = 0;
+    }
+    if (warp == 8) {
+        sm100::tmem_alloc(sm100::smem_u32(&s_tmem), 4 * W);
+        sm100::tmem_relinquish();
+    }
+    sm100::tc_fence_before();
+    Tiles<kWideThreads> tiles;
+    tiles.scan(rows, kTileTokens);
+    sm100::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int nblk = (C + W - 1) / W;
+    const int64_t items = tiles.total * nblk;
+    const int64_t it_lo = items * blockIdx.x / gridDim.x, it_hi = items * (blockIdx.x + 1) / gridDim.x;
+    uint32_t use = 0;      // column blocks this CTA has been through: buffer use & 1, phase use / 2
+    bool waited = false;
+    bool alive = true;
+    for (int64_t it = it_lo; it < it_hi;) {
+        const Tile tile = tiles.find(it / nblk);
+        const int b_lo = static_cast<int>(it % nblk);
+        const int b_hi = static_cast<int>(min(static_cast<int64_t>(nblk), b_lo + (it_hi - it)));
+        const int nb = b_hi - b_lo;
+        if (tid < kTileTokens) {
+            const int tok = (tid < tile.count) ? __ldg(rows.tokens + tile.p0 + tid) : -1;
+            s_tok[tid] = (tok >= 0 && tok < rows.T) ? tok : -1;
+        }
+        __syncthreads();
+        if (warp > 8) {
+            // producers: a column block's base rows, W / 4 pieces each
+            constexpr int kAt = 128 / W;  // rows per warp and instruction
+            const int pc = lane % (W / 4) * 4;
+            for (int j = 0; j < nb && alive; ++j) {
+                const uint32_t u = use + j;
+                const int b = u & 1;
+                if (u >= 2) alive = wait(bar(kFree, b), (u >> 1) - 1);
+                const int c = (b_lo + j) * W + pc;
+                if (base && alive && c < C) {
+#pragma unroll 8
+                    for (int r = (warp - 9) * kAt + lane / (W / 4); r < kTileTokens; r += 4 * kAt) {
+                        const int tok = s_tok[r];
+                        if (tok >= 0)
+                            cp_async16(sm100::smem_u32(bufs + (b * kTileTokens + r) * P + pc * 4),
+                                       base + tok * ld_base + c, true);
+                    }
+                }
+                cp_async_arrive(bar(kBaseIn, b));
+            }
+        } else {
+            if (warp < 8) {
+                // the terms of v: row tid % 128, every other 8 ranks
+                if (!waited) wait_previous();
+                waited = true;
+                const int row = tid & 127;
+                const bool in = row < tile.count;
+                const float* src = v + static_cast<int64_t>(tile.p0 + row) * R;
+                float t[RP / 16][8];  // all loads before the first use
+#pragma unroll
+                for (int i = 0; i < RP / 16; ++i) {
+                    const int r = (tid >> 7) * 8 + 16 * i;
+#pragma unroll
+                    for (int u = 0; u < 8; u += 4) {
+                        if (R % 4 == 0) {
+                            const float4 q4 = (in && r + u < R) ? __ldcg(reinterpret_cast<const float4*>(src + r + u))
+                                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                            t[i][u] = q4.x;
+                            t[i][u + 1] = q4.y;
+                            t[i][u + 2] = q4.z;
+                            t[i][u + 3] = q4.w;
+                        } else {
+#pragma unroll
+                            for (int w4 = 0; w4 < 4; ++w4)
+                                t[i][u + w4] = (in && r + u + w4 < R) ? __ldcg(src + r + u + w4) : 0.0f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < RP / 16; ++i) {
+                    uint4 term[3];
+                    split3_pair(t[i][0], t[i][1], term[0].x, term[1].x, term[2].x);
+                    split3_pair(t[i][2], t[i][3], term[0].y, term[1].y, term[2].y);
+                    split3_pair(t[i][4], t[i][5], term[0].z, term[1].z, term[2].z);
+                    split3_pair(t[i][6], t[i][7], term[0].w, term[1].w, term[2].w);
+#pragma unroll
+                    for (int sp = 0; sp < 3; ++sp) {
+                        const int col = sp * RP + (tid >> 7) * 8 + 16 * i;
+                        *reinterpret_cast<uint4*>(mem + (col >> 6) * kTileTokens * 128 + row * 128 +
+                                                  ((((col & 63) >> 3) ^ (row & 7)) << 4)) = term[sp];
+                    }
+                }
+                sm100::fence_proxy_async_smem();
+            }
+            auto load_slab = [&](int j) {
+                if (lane != 0 || j >= nb) return;
+                const int sl = (use + j) & 1;
+                sm100::mbar_arrive_expect_tx(bar(kSlabIn, sl), kSlab);
+                for (int h = 0; h < W / 64; ++h)
+                    sm100::tma_load_3d(sm100::smem_u32(slabs + sl * kSlab + h * RP * 128), &wmap,
+                                       ((b_lo + j) * W + 64 * h) * 2, 0, tile.a, bar(kSlabIn, sl));
+            };
+            if (warp == 8) {  // the slabs of the tile before are all used
+                load_slab(0);
+                load_slab(1);
+            }
+            asm volatile("bar.sync 1, 288;" ::: "memory");  // epilogue groups and issuer: v is in place
+            if (warp == 8) {
+                constexpr uint32_t idesc = idesc_bf16_f32(kTileTokens, W, 0, 1);
+                for (int j = 0; j < nb && alive; ++j) {
+                    const uint32_t u = use + j;
+                    const int sl = u & 1, d = u & 3;
+                    if (u >= 4) alive = wait(bar(kRead, d), (u >> 2) - 1);
+                    alive = alive && wait(bar(kSlabIn, sl), u >> 1);
+                    alive = __all_sync(0xFFFFFFFFu, alive);
+                    if (!alive) break;
+                    if (lane == 0) {
+                        sm100::tc_fence_after();
+                        const uint64_t dw = sw128_mnmajor_desc(sm100::smem_u32(slabs + sl * kSlab), RP * 128);
+#pragma unroll
+                        for (int sp = 2; sp >= 0; --sp)  // the small terms first
+#pragma unroll
+                            for (int k = 0; k < RP / 16; ++k) {
+                                const uint64_t dv = sw128_kmajor_desc_at(sm100::smem_u32(mem), sp * RP + k * 16);
+                                mma_f16_ss(tmem + d * W, dv, dw + k * 2048 / 16, idesc, (sp != 2 || k != 0) ? 1u : 0u);
+                            }
+                        sm100::mma_commit(bar(kReady, d));
+                        sm100::mma_commit(bar(kSlabUsed, sl));
+                    }
+                    __syncwarp();
+                    if (j > 0) {  // the slab before is free: fetch the one after this
+                        alive = wait(bar(kSlabUsed, sl ^ 1), (u - 1) >> 1);
+                        load_slab(j + 1);
+                    }
+                }
+                if (alive) alive = wait(bar(kSlabUsed, (use + nb - 1) & 1), (use + nb - 1) >> 1);
+            } else {
+                const int b = warp >> 2;
+                const int row = tid & 127;
+                const int tok = s_tok[row];
+                const float f = scales ? __ldg(scales + tile.a) : 1.0f;
+                uint8_t* const mine = bufs + (b * kTileTokens + row) * P;
+                for (int j = (b ^ use) & 1; j < nb; j += 2) {
+                    const uint32_t u = use + j;
+                    const int c0 = (b_lo + j) * W;
+                    const int width = min(W, C - c0);
+                    const int d = u & 3;
+                    alive = alive && wait(bar(kReady, d), u >> 2);
+                    alive = alive && wait(bar(kBaseIn, b), u >> 1);
+                    if (!alive) {  // a wait ran out: the row says so
+                        if (tok >= 0)
+                            for (int c = 0; c < width; ++c) out[tok * ld_out + c0 + c] = NAN;
+                        continue;
+                    }
+                    __syncwarp();
+                    sm100::tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < W; c += 32) {
+                        uint32_t t[32];
+                        sm100::tmem_ld32_issue(tmem + (static_cast<uint32_t>(warp & 3) << 21) + d * W + c, t);
+                        sm100::tmem_ld_wait(t);
+#pragma unroll
+                        for (int q4 = 0; q4 < 8; ++q4) {
+                            float4* at = reinterpret_cast<float4*>(mine + (c + 4 * q4) * 4);
+                            const float4 o = base ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+                            *at = make_float4(fmaf(f, __uint_as_float(t[4 * q4]), o.x),
+                                              fmaf(f, __uint_as_float(t[4 * q4 + 1]), o.y),
+                                              fmaf(f, __uint_as_float(t[4 * q4 + 2]), o.z),
+                                              fmaf(f, __uint_as_float(t[4 * q4 + 3]), o.w));
+                        }
+                    }
+                    sm100::tc_fence_before();
+                    sm100::mbar_arrive(bar(kRead, d));
+                    __syncwarp();
+                    constexpr int kAt = 128 / W;  // rows per instruction
+                    const int c = lane % (W / 4) * 4;
+                    if (c < width) {
+#pragma unroll 4
+                        for (int r = (warp & 3) * 32 + lane / (W / 4); r < (warp & 3) * 32 + 32; r += kAt) {
+                            const int tk = s_tok[r];
+                            if (tk < 0) continue;
+                            const float4 o = *reinterpret_cast<const float4*>(bufs + (b * kTileTokens + r) * P + c * 4);
+                            *reinterpret_cast<float4*>(out + tk * ld_out + c0 + c) = o;
+                            if (out_bf16)
+                                *reinterpret_cast<uint2*>(out_bf16 + static_cast<int64_t>(tk) * C + c0 + c) =
+                                    make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+                        }
+                    }
+                    sm100::mbar_arrive(bar(kFree, b));
+                }
+            }
+        }
+        __syncthreads();  // the tile's v and token list are free
+        use += nb;
+        it += nb;
+    }
+    if (!waited) wait_previous();  // this kernel never ends before the one it follows
+    // after a wait that ran out: copies in flight land before the block ends
+    if (warp > 8) cp_async_wait_all();
+    if (warp == 8 && lane == 0 && s_abort) {
+        __shared__ int s_drain;
+        s_drain = 0;
+        for (int b = 0; b < 2; ++b)
+            sm100::mbar_wait_bounded(bar(kSlabIn, b), (((use + 1) >> 1) - 1) & 1, &s_drain, 1000000ull);
+    }
+    __syncthreads();
+    if (warp == 8) {
+        sm100::tc_fence_after();
+        sm100::tmem_dealloc(tmem, 4 * W);
+    }
+}
+
 // ------------------------------------------------------------------- outer
 //
-// d[a, r, c] = f_a sum_p v[p, r] x[tok, c], 64 ranks times 256 columns per
+// d[a, r, c] = f_a sum_p v[p, r] x[tok, c], 64 ranks times 128 columns per
 // cluster on tcgen05; tokens are the K of the product, dealt in equal runs to
 // the cluster's blocks.  Both operands lie in shared memory token by token,
 // 64 values (128 bytes, 128-byte swizzle) per token and panel, so they are
-// MN-major: x comes in by cp.async (gathered rows), the three terms of v are
-// written by the threads, which split them on the way.  The three products
-// share the accumulator; it is moved to FP32 registers every kOuterChain
-// stages, so no long sum is left to the tensor core's rounding.  Two blocks
-// per SM cover each other's waits.  The blocks' sums are joined in block
+// MN-major.  Four producer warps bring in the x rows (gathered) and the raw
+// rows of v by cp.async; four more split v into its three terms, and move the
+// accumulator to FP32 registers every kOuterChain stages (two TMEM buffers in
+// turn), so no long sum is left to the tensor core's rounding; one thread
+// issues the MMAs, three per 16 tokens into one accumulator.  Two blocks per
+// SM cover each other's start and end.  The blocks' sums are joined in block
 // order.
-constexpr int kOuterThreads = 128;
+constexpr int kOuterThreads = 288;
 constexpr int kOuterRanks = 64;
-constexpr int kOuterCols = 256;
+constexpr int kOuterCols = 128;
 constexpr int kOuterTokens = 32;   // per stage
 constexpr int kOuterStages = 3;
-constexpr int kOuterChain = 8;
+constexpr int kOuterChain = 4;
 constexpr int kOuterPanel = kOuterTokens * 128;
-constexpr int kOuterStageBytes = (kOuterCols / 64 + 3) * kOuterPanel;  // four panels of x, three of v
-constexpr int kOuterPitch = kOuterCols + 4;                            // floats per rank row of the block's sums
+constexpr int kOuterRawPitch = kOuterRanks * 4 + 16;  // bytes
+constexpr int kOuterX = 0, kOuterV = (kOuterCols / 64) * kOuterPanel, kOuterRaw = kOuterV + 3 * kOuterPanel;
+constexpr int kOuterStageBytes = (kOuterRaw + kOuterTokens * kOuterRawPitch + 1023) / 1024 * 1024;
+constexpr int kOuterPitch = kOuterCols + 4;  // floats per rank row of the block's sums
 constexpr int kOuterSmem = 1024 + kOuterStages * kOuterStageBytes;
 static_assert(kOuterRanks * kOuterPitch * 4 <= kOuterStages * kOuterStageBytes, "the sums reuse the ring");
 
-// Shared-memory matrix descriptor of an MN-major operand in the 128-byte
-// swizzle: panels of 64 MN values (128-byte rows, one per K index), 8 K rows
-// per 1024-byte atom (stride offset), panels `panel` bytes apart (leading
-// offset).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t panel)
-{
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(panel >> 4) << 16;
-    d |= static_cast<uint64_t>(1024u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
-}
-
-__global__ void __launch_bounds__(kOuterThreads)
+__global__ void __launch_bounds__(kOuterThreads, 2)
     lora_outer_kernel(LoraRows rows, int R, int rblocks, LoraOuter pa, LoraOuter pb, int ablocks)
 {
     constexpr int S = kOuterStages;
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t s_bar[S];
+    __shared__ __align__(8) uint64_t s_full[S], s_split[S], s_empty[S], s_ready[2], s_read[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     cg::cluster_group cluster = cg::this_cluster();
@@ -662,9 +1032,6 @@ __global__ void __launch_bounds__(kOuterThreads)
     const int rank = static_cast<int>(cluster.block_rank());
     const int blk = static_cast<int>(blockIdx.x) / nc;
     const bool first = blk < ablocks;
-    const float* const pv = first ? pa.v : pb.v;
-    const uint16_t* const px = first ? pa.x : pb.x;
-    const int64_t ldx = first ? pa.ldx : pb.ldx;
     const int C = first ? pa.C : pb.C;
     const int c0 = (first ? blk : blk - ablocks) * kOuterCols;
     const int a = blockIdx.y / rblocks;
@@ -673,12 +1040,20 @@ __global__ void __launch_bounds__(kOuterThreads)
     uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
     const uint32_t ring_s = sm100::smem_u32(ring);
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) sm100::mbar_init(sm100::smem_u32(&s_bar[i]), 1);
+        for (int i = 0; i < S; ++i) {
+            sm100::mbar_init(sm100::smem_u32(&s_full[i]), 128);
+            sm100::mbar_init(sm100::smem_u32(&s_split[i]), 128);
+            sm100::mbar_init(sm100::smem_u32(&s_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            sm100::mbar_init(sm100::smem_u32(&s_ready[i]), 1);
+            sm100::mbar_init(sm100::smem_u32(&s_read[i]), 128);
+        }
         sm100::fence_barrier_init();
         s_abort = 0;
     }
-    if (warp == 0) {
-        sm100::tmem_alloc(sm100::smem_u32(&s_tmem), kOuterCols);
+    if (warp == 8) {
+        sm100::tmem_alloc(sm100::smem_u32(&s_tmem), 2 * kOuterCols);
         sm100::tmem_relinquish();
     }
     sm100::tc_fence_before();
@@ -693,141 +1068,167 @@ __global__ void __launch_bounds__(kOuterThreads)
     const int s_lo = static_cast<int>(static_cast<int64_t>(stages) * rank / nc);
     const int mine = static_cast<int>(static_cast<int64_t>(stages) * (rank + 1) / nc) - s_lo;
     const int p0 = lo + s_lo * kOuterTokens;
-    // x: piece ch (8 columns) of panel j, token rows row0 and row0 + 16
-    const int ch = tid & 7, row0 = tid >> 3;
-    const uint32_t swz = static_cast<uint32_t>(ch ^ (row0 & 7)) << 4;
-    auto load_x = [&](int i) {
-        if (i < mine) {
-            const uint32_t dst = ring_s + (i % S) * kOuterStageBytes + row0 * 128 + swz;
+    auto wait = [&](uint64_t* b, int phase) {
+        return sm100::mbar_wait_bounded(sm100::smem_u32(b), phase & 1, &s_abort, kTileWaitNs);
+    };
+    wait_previous();  // dv
+    float sum[kOuterCols / 64][32];
+    if (warp < 4) {
+        // v: token vt, ranks vr .. vr + 15 of the block's 64
+        const int vt = tid >> 2, vr = (tid & 3) * 16;
+#pragma unroll
+        for (int j = 0; j < kOuterCols / 64; ++j)
+#pragma unroll
+            for (int u = 0; u < 32; ++u) sum[j][u] = 0.0f;
+        auto promote = [&](int c) {
+            if (!wait(&s_ready[c & 1], c >> 1)) return;
+            __syncwarp();
+            sm100::tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < kOuterCols / 64; ++j) {
+                uint32_t t[32];
+                sm100::tmem_ld16x256_x8_issue(
+                    tmem + (static_cast<uint32_t>(warp) << 21) + (c & 1) * kOuterCols + j * 64, t);
+                sm100::tmem_ld_wait(t);
+#pragma unroll
+                for (int u = 0; u < 32; ++u) sum[j][u] += __uint_as_float(t[u]);
+            }
+            sm100::tc_fence_before();
+            sm100::mbar_arrive(sm100::smem_u32(&s_read[c & 1]));
+        };
+        int done = 0;  // chains in registers
+        for (int i = 0; i < mine; ++i) {
+            // the stage's MMAs of S stages ago are complete (its raw rows too
+            // are only there since), and with them a chain that ended there
+            if (!wait(&s_full[i % S], i / S)) break;
+            if (i >= S && (i - S + 1) % kOuterChain == 0) promote(done++);
+            uint8_t* const st = ring + (i % S) * kOuterStageBytes;
+            const float4* raw = reinterpret_cast<const float4*>(st + kOuterRaw + vt * kOuterRawPitch + vr * 4);
+            uint8_t* const dst = st + kOuterV + vt * 128;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float4 p = raw[2 * u], q = raw[2 * u + 1];
+                uint4 h, m, l;
+                split3_pair(p.x, p.y, h.x, m.x, l.x);
+                split3_pair(p.z, p.w, h.y, m.y, l.y);
+                split3_pair(q.x, q.y, h.z, m.z, l.z);
+                split3_pair(q.z, q.w, h.w, m.w, l.w);
+                const int at = ((vr / 8 + u) ^ (vt & 7)) << 4;
+                *reinterpret_cast<uint4*>(dst + at) = h;
+                *reinterpret_cast<uint4*>(dst + kOuterPanel + at) = m;
+                *reinterpret_cast<uint4*>(dst + 2 * kOuterPanel + at) = l;
+            }
+            sm100::fence_proxy_async_smem();
+            sm100::mbar_arrive(sm100::smem_u32(&s_split[i % S]));
+        }
+        const int chains = (mine + kOuterChain - 1) / kOuterChain;
+        while (done < chains && !*static_cast<volatile int*>(&s_abort)) promote(done++);
+    } else if (warp < 8) {
+        const float* const pv = first ? pa.v : pb.v;
+        const uint16_t* const px = first ? pa.x : pb.x;
+        const int64_t ldx = first ? pa.ldx : pb.ldx;
+        const int pt = tid - 128;
+        // x: piece ch (8 columns) of the panels, token rows row0 and row0 + 16
+        const int ch = pt & 7, row0 = pt >> 3;
+        const uint32_t swz = static_cast<uint32_t>(ch ^ (row0 & 7)) << 4;
+        // v: ranks r4 .. r4 + 3 of token rows v0 + 8 h
+        const int r4 = (pt & 15) * 4, v0 = pt >> 4;
+        int next[kOuterTokens / 16];  // token rows of the next stage
+        auto load_tokens = [&](int i) {
 #pragma unroll
             for (int h = 0; h < kOuterTokens / 16; ++h) {
-                const int p = p0 + i * kOuterTokens + row0 + 16 * h;
-                const int tok = p < hi ? __ldg(rows.tokens + p) : -1;
+                const int at = p0 + i * kOuterTokens + row0 + 16 * h;
+                next[h] = at < hi ? __ldg(rows.tokens + at) : -1;
+            }
+        };
+        load_tokens(0);
+        for (int i = 0; i < mine; ++i) {
+            int cur[kOuterTokens / 16];
+#pragma unroll
+            for (int h = 0; h < kOuterTokens / 16; ++h) cur[h] = next[h];
+            load_tokens(i + 1);
+            if (i >= S && !wait(&s_empty[i % S], i / S - 1)) break;
+            const uint32_t st = ring_s + (i % S) * kOuterStageBytes;
+            const int p = p0 + i * kOuterTokens;
+#pragma unroll
+            for (int h = 0; h < kOuterTokens / 16; ++h) {
+                const int tok = cur[h];
                 const bool row = tok >= 0 && tok < T;
                 const uint16_t* src = px + (row ? tok * ldx : 0) + c0 + ch * 8;
 #pragma unroll
                 for (int j = 0; j < kOuterCols / 64; ++j) {
                     const bool ok = row && c0 + j * 64 + ch * 8 < C;
-                    cp_async16(dst + j * kOuterPanel + h * 2048, ok ? src + j * 64 : px, ok);
+                    cp_async16(st + kOuterX + j * kOuterPanel + (row0 + 16 * h) * 128 + swz, ok ? src + j * 64 : px, ok);
                 }
             }
-        }
-        cp_async_commit();
-    };
-    // v: token vt, ranks vr .. vr + 15 of the block's 64
-    const int vt = tid >> 2, vr = (tid & 3) * 16;
-    float va[16];
-    auto load_v = [&](int i) {
-        const int p = p0 + i * kOuterTokens + vt;
-        const bool row = i < mine && p < hi;
-        const float* src = pv + static_cast<int64_t>(p) * R + r0 + vr;
-        if (R % 4 == 0) {
 #pragma unroll
-            for (int u = 0; u < 16; u += 4) {
-                const float4 t = (row && r0 + vr + u < R) ? __ldcg(reinterpret_cast<const float4*>(src + u))
-                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-                va[u] = t.x;
-                va[u + 1] = t.y;
-                va[u + 2] = t.z;
-                va[u + 3] = t.w;
+            for (int h = 0; h < kOuterTokens / 8; ++h) {
+                const int row = v0 + 8 * h;
+                const uint32_t dst = st + kOuterRaw + row * kOuterRawPitch + r4 * 4;
+                const float* src = pv + static_cast<int64_t>(p + row) * R + r0 + r4;
+                if (R % 4 == 0) {
+                    const bool ok = p + row < hi && r0 + r4 < R;
+                    cp_async16(dst, ok ? src : pv, ok);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const bool ok = p + row < hi && r0 + r4 + u < R;
+                        cp_async4(dst + 4 * u, ok ? src + u : pv, ok);
+                    }
+                }
             }
-        } else {
-#pragma unroll
-            for (int u = 0; u < 16; ++u) va[u] = (row && r0 + vr + u < R) ? __ldcg(src + u) : 0.0f;
+            cp_async_arrive(sm100::smem_u32(&s_full[i % S]));
         }
-    };
-    auto store_v = [&](int i) {
-        uint8_t* const dst = ring + (i % S) * kOuterStageBytes + (kOuterCols / 64) * kOuterPanel + vt * 128;
+        cp_async_wait_all();
+    } else {
+        constexpr uint32_t idesc = idesc_bf16_f32(kOuterRanks, kOuterCols, 1, 1);
+        for (int i = 0; i < mine; ++i) {
+            const int c = i / kOuterChain;
+            bool ok = true;
+            if (i % kOuterChain == 0 && c >= 2) ok = wait(&s_read[c & 1], (c >> 1) - 1);
+            ok = ok && wait(&s_full[i % S], i / S) && wait(&s_split[i % S], i / S);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (lane == 0) {
+                sm100::fence_proxy_async_smem();
+                sm100::tc_fence_after();
+                const uint32_t st = ring_s + (i % S) * kOuterStageBytes;
+                const uint64_t dx = sw128_mnmajor_desc(st + kOuterX, kOuterPanel);
+                const uint64_t dv = sw128_mnmajor_desc(st + kOuterV, kOuterPanel);
 #pragma unroll
-        for (int u = 0; u < 16; u += 8) {
-            uint4 h, m, l;
-            split3_pair(va[u], va[u + 1], h.x, m.x, l.x);
-            split3_pair(va[u + 2], va[u + 3], h.y, m.y, l.y);
-            split3_pair(va[u + 4], va[u + 5], h.z, m.z, l.z);
-            split3_pair(va[u + 6], va[u + 7], h.w, m.w, l.w);
-            const int at = (((vr + u) >> 3) ^ (vt & 7)) << 4;
-            *reinterpret_cast<uint4*>(dst + at) = h;
-            *reinterpret_cast<uint4*>(dst + kOuterPanel + at) = m;
-            *reinterpret_cast<uint4*>(dst + 2 * kOuterPanel + at) = l;
+                for (int kk = 0; kk < kOuterTokens / 16; ++kk)
+#pragma unroll
+                    for (int sp = 2; sp >= 0; --sp)  // 16 token rows are 2048 bytes
+                        mma_f16_ss(tmem + (c & 1) * kOuterCols, dv + (sp * kOuterPanel + kk * 2048) / 16,
+                                   dx + kk * 2048 / 16, idesc,
+                                   (i % kOuterChain != 0 || kk != 0 || sp != 2) ? 1u : 0u);
+                sm100::mma_commit(sm100::smem_u32(&s_empty[i % S]));
+                if (i % kOuterChain == kOuterChain - 1 || i == mine - 1)
+                    sm100::mma_commit(sm100::smem_u32(&s_ready[c & 1]));
+            }
+            __syncwarp();
         }
-    };
-    float sum[kOuterCols / 64][32];
-#pragma unroll
-    for (int j = 0; j < kOuterCols / 64; ++j)
-#pragma unroll
-        for (int u = 0; u < 32; ++u) sum[j][u] = 0.0f;
-    bool alive = true;
-    auto wait_stage = [&](int i) {  // the MMAs of stage i are complete
-        alive = alive && sm100::mbar_wait_bounded(sm100::smem_u32(&s_bar[i % S]), (i / S) & 1,
-                                                  reinterpret_cast<volatile int*>(&s_abort), kTileWaitNs);
-    };
-    auto promote = [&]() {
-        sm100::tc_fence_after();
-#pragma unroll
-        for (int j = 0; j < kOuterCols / 64; ++j) {
-            uint32_t t[32];
-            sm100::tmem_ld16x256_x8_issue(tmem + (static_cast<uint32_t>(warp) << 21) + j * 64, t);
-            sm100::tmem_ld_wait(t);
-#pragma unroll
-            for (int u = 0; u < 32; ++u) sum[j][u] += __uint_as_float(t[u]);
-        }
-        sm100::tc_fence_before();
-    };
-    constexpr uint32_t idesc = idesc_bf16_f32(kOuterRanks, kOuterCols, 1, 1);
-    load_x(0);
-    load_x(1);
-    wait_previous();  // dv
-    load_v(0);
-    for (int i = 0; i < mine; ++i) {
-        store_v(i);
-        load_v(i + 1);
-        if (i > 0 && i % kOuterChain == 0) {
-            wait_stage(i - 1);
-            promote();
-        }
-        cp_async_wait<1>();
-        sm100::fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0 && alive) {
-            sm100::tc_fence_after();
-            const uint32_t st = ring_s + (i % S) * kOuterStageBytes;
-            const uint64_t dx = sw128_mnmajor_desc(st, kOuterPanel);
-            const uint64_t dv = sw128_mnmajor_desc(st + (kOuterCols / 64) * kOuterPanel, kOuterPanel);
-#pragma unroll
-            for (int kk = 0; kk < kOuterTokens / 16; ++kk)
-#pragma unroll
-                for (int sp = 2; sp >= 0; --sp)  // 16 token rows are 2048 bytes
-                    mma_f16_ss(tmem, dv + (sp * kOuterPanel + kk * 2048) / 16, dx + kk * 2048 / 16, idesc,
-                               (i % kOuterChain != 0 || kk != 0 || sp != 2) ? 1u : 0u);
-            sm100::mma_commit(sm100::smem_u32(&s_bar[i % S]));
-        }
-        if (i > 0) wait_stage(i - 1);
-        load_x(i + 2);
     }
-    if (mine > 0) {
-        wait_stage(mine - 1);
-        promote();
-    }
-    cp_async_wait<0>();
-    __syncthreads();
-    if (warp == 0) {
+    __syncthreads();  // every chain is read: the MMAs and the ring are done with
+    if (warp == 8) {
         sm100::tc_fence_after();
-        sm100::tmem_dealloc(tmem, kOuterCols);
+        sm100::tmem_dealloc(tmem, 2 * kOuterCols);
     }
     // the block's sums: lane l holds ranks 16 warp + l / 4 (+ 8), columns
     // 64 j + 8 i + 2 (l % 4) and + 1; a wait that ran out leaves NaN
     float* const part = reinterpret_cast<float*>(ring);
+    if (warp < 4) {
+        const bool bad = s_abort != 0;
 #pragma unroll
-    for (int j = 0; j < kOuterCols / 64; ++j)
+        for (int j = 0; j < kOuterCols / 64; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float2 t = make_float2(sum[j][4 * i + 2 * h], sum[j][4 * i + 2 * h + 1]);
-                if (!alive) t = make_float2(NAN, NAN);
-                *reinterpret_cast<float2*>(part + (16 * warp + lane / 4 + 8 * h) * kOuterPitch + 64 * j + 8 * i +
-                                           2 * (lane % 4)) = t;
-            }
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float2*>(part + (16 * warp + lane / 4 + 8 * h) * kOuterPitch + 64 * j + 8 * i +
+                                               2 * (lane % 4)) =
+                        bad ? make_float2(NAN, NAN)
+                            : make_float2(sum[j][4 * i + 2 * h], sum[j][4 * i + 2 * h + 1]);
+    }
     cluster.sync();
     const float* const scales = first ? pa.scales : pb.scales;
     const float f = scales ? __ldg(scales + a) : 1.0f;
@@ -889,8 +1290,17 @@ cudaError_t allow_smem(K kernel, size_t bytes)
 int cluster_size(int64_t units, int steps, int least, int sm_count)
 {
     int nc = 1;
-    while (nc < 8 && units * nc < 2 * sm_count && steps >= 2 * nc * least) nc *= 2;
+    while (nc < 8 && units * 2 * nc <= 2 * sm_count && steps >= 2 * nc * least) nc *= 2;
     return nc;
+}
+
+// Rank rows [n, R, C] BF16 as bytes, boxes of 64 columns times RP ranks of one
+// adapter (zeros past R and C).
+bool rank_map(CUtensorMap* map, const LoraRows& rows, const uint16_t* w, int R, int C, int RP)
+{
+    const uint64_t dims[3] = {static_cast<uint64_t>(C) * 2, static_cast<uint64_t>(R), static_cast<uint64_t>(rows.n)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(C) * 2, static_cast<uint64_t>(R) * C * 2};
+    return make_tmap_u8(map, w, 3, dims, strides, RP);
 }
 
 template <int MR>
@@ -910,23 +1320,39 @@ cudaError_t shrink_tile(const LoraRows& rows, const uint16_t* x, int64_t ldx, in
 {
     const int64_t units = max_tiles(rows.T, rows.n, kTileTokens);
     const int nc = cluster_size(units, (C + 63) / 64, 4, sm_count);
+    CUtensorMap map;
+    if (!rank_map(&map, rows, w, R, C, RP)) return cudaErrorNotSupported;
     cudaError_t err = allow_smem(lora_shrink_tile_kernel<RP>, tile_smem(RP));
     if (err != cudaSuccess) return err;
     Launch l(units * nc, kTileThreads, tile_smem(RP), s, nc, false);
-    return cudaLaunchKernelEx(&l.cfg, lora_shrink_tile_kernel<RP>, rows, x, ldx, C, w, R, scales, v);
+    return cudaLaunchKernelEx(&l.cfg, lora_shrink_tile_kernel<RP>, map, rows, x, ldx, C, R, scales, v);
 }
 
-template <int KS, int NW, int BT>
+template <int RP>
+cudaError_t expand_tile(const LoraRows& rows, const float* v, int R, const uint16_t* w, int C, const float* scales,
+                        const float* base, int64_t ld_base, float* out, int64_t ld_out, uint16_t* out_bf16,
+                        int sm_count, cudaStream_t s)
+{
+    CUtensorMap map;
+    if (!rank_map(&map, rows, w, R, C, RP)) return cudaErrorNotSupported;
+    cudaError_t err = allow_smem(lora_expand_tile_kernel<RP>, wide_smem(RP));
+    if (err != cudaSuccess) return err;
+    Launch l(sm_count, kWideThreads, wide_smem(RP), s, 0, true);
+    return cudaLaunchKernelEx(&l.cfg, lora_expand_tile_kernel<RP>, map, rows, v, R, C, scales, base, ld_base, out,
+                              ld_out, out_bf16);
+}
+
+template <int KS, int NW, int BT, int RING>
 cudaError_t expand(const LoraRows& rows, const float* v, int R, const uint16_t* w, int C, const float* scales,
                    const float* base, int64_t ld_base, float* out, int64_t ld_out, uint16_t* out_bf16, cudaStream_t s)
 {
     const int cols = kExpandThreads / 32 * 8 * NW;
     const int cblocks = (C + cols - 1) / cols;
-    constexpr int smem = expand_smem<KS, NW, BT>();
-    cudaError_t err = allow_smem(lora_expand_kernel<KS, NW, BT>, smem);
+    constexpr int smem = expand_smem<KS, NW, BT, RING>();
+    cudaError_t err = allow_smem(lora_expand_kernel<KS, NW, BT, RING>, smem);
     if (err != cudaSuccess) return err;
     Launch l(max_tiles(rows.T, rows.n, BT) * cblocks, kExpandThreads, smem, s, 0, true);
-    return cudaLaunchKernelEx(&l.cfg, lora_expand_kernel<KS, NW, BT>, rows, v, R, w, C, cblocks, scales, base, ld_base,
+    return cudaLaunchKernelEx(&l.cfg, lora_expand_kernel<KS, NW, BT, RING>, rows, v, R, w, C, cblocks, scales, base, ld_base,
                               out, ld_out, out_bf16);
 }
 
@@ -952,10 +1378,21 @@ cudaError_t launch_lora_expand(const LoraRows& rows, const float* v, int R, cons
                                const float* scales, const float* base, int64_t ld_base, float* out, int64_t ld_out,
                                uint16_t* out_bf16, cudaStream_t s)
 {
-    if (R <= 16) return expand<1, 8, 64>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
-    if (R <= 32) return expand<2, 8, 64>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
-    if (R <= 64) return expand<4, 8, 64>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
-    return expand<8, 4, 32>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
+    // Ranks above 32 with many tokens per adapter and enough rows to fill the
+    // GPU: the tcgen05 kernel (16384 x 6144, rank 64: 172 us against 220;
+    // 4096 x 5120: 55 against 64; 2048 x 2048: 28.5 against 25).  Up to rank
+    // 32 the register kernel is ahead (rank 16: 136 us against 153).
+    if (R > 32 && rows.T >= 64 * static_cast<int64_t>(rows.n) && rows.T * C >= (int64_t(1) << 24)) {
+        DeviceInfo di;
+        if (!device_info(&di)) return cudaErrorUnknown;
+        return R <= 64 ? expand_tile<64>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, di.sm_count, s)
+                       : expand_tile<128>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, di.sm_count,
+                                          s);
+    }
+    if (R <= 16) return expand<1, 8, 64, 3>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
+    if (R <= 32) return expand<2, 8, 64, 3>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
+    if (R <= 64) return expand<4, 8, 64, 2>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
+    return expand<8, 4, 32, 3>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
 }
 
 cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, const LoraOuter& b, cudaStream_t s)
