@@ -436,6 +436,18 @@ int moe_route_backward(const float* logits, int64_t T, int E, const int32_t* top
 
 namespace {
 
+// Workspace of the adapters' backward: dv [T, rank] FP32, then the BF16 terms
+// of dv and of v.
+size_t lora_ws_layout(int64_t T, int rank, size_t* off_dv_terms, size_t* off_v_terms)
+{
+    const int64_t t = T > 0 ? T : 1;
+    size_t o = align_up(static_cast<size_t>(t) * rank * 4, 256);
+    *off_dv_terms = o;
+    o = align_up(o + lora_terms_bytes(t, rank), 256);
+    *off_v_terms = o;
+    return align_up(o + lora_terms_bytes(t, rank), 256);
+}
+
 bool row_major(int64_t ld, int cols, int unit) { return ld >= cols && ld % unit == 0; }
 
 // Sizes shared by the adapter entry points.
@@ -471,7 +483,7 @@ int moe_lora(const uint16_t* x, int64_t ld_x, int64_t T, int K, const uint16_t* 
     if (int r = check_device()) return r;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LoraRows rows{T, n_adapters, adapter_offsets, sorted_tokens};
-    cudaError_t err = launch_lora_shrink(rows, x, ld_x, K, lora_a, rank, nullptr, v, s);
+    cudaError_t err = launch_lora_shrink(rows, x, ld_x, K, lora_a, rank, nullptr, v, nullptr, nullptr, nullptr, s);
     if (err == cudaSuccess)
         err = launch_lora_expand(rows, v, rank, lora_b, N, scales, base, ld_base, out, ld_out, out_bf16, s);
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_lora");
@@ -480,7 +492,8 @@ int moe_lora(const uint16_t* x, int64_t ld_x, int64_t T, int K, const uint16_t* 
 size_t moe_lora_backward_workspace_bytes(int64_t T, int rank)
 {
     if (T < 0 || rank < 1) return 0;
-    return align_up(static_cast<size_t>(T > 0 ? T : 1) * rank * 4, 256);
+    size_t a, b;
+    return lora_ws_layout(T, rank, &a, &b);
 }
 
 int moe_lora_backward(const uint16_t* x, int64_t ld_x, int64_t T, int K, const uint16_t* lora_a,
@@ -504,14 +517,18 @@ int moe_lora_backward(const uint16_t* x, int64_t ld_x, int64_t T, int K, const u
     if (int r = check_device()) return r;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LoraRows rows{T, n_adapters, adapter_offsets, sorted_tokens};
+    size_t off_dvt, off_vt;
+    lora_ws_layout(T, rank, &off_dvt, &off_vt);
     float* dv = static_cast<float*>(ws);
+    uint16_t* dv_terms = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + off_dvt);
+    uint16_t* v_terms = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + off_vt);
     cudaError_t err = cudaSuccess;
-    if (T > 0) err = launch_lora_shrink(rows, dout, ld_dout, N, lora_b, rank, scales, dv, s);
+    if (T > 0) err = launch_lora_shrink(rows, dout, ld_dout, N, lora_b, rank, scales, dv, dv_terms, v, v_terms, s);
     if (err == cudaSuccess && T > 0 && dx)
         err = launch_lora_expand(rows, dv, rank, lora_a, K, nullptr, dx_base, ld_dx_base, dx, ld_dx, nullptr, s);
     if (err == cudaSuccess)
-        err = launch_lora_outer(rows, rank, LoraOuter{dv, x, ld_x, K, nullptr, d_a},
-                                LoraOuter{v, dout, ld_dout, N, scales, d_b}, s);
+        err = launch_lora_outer(rows, rank, LoraOuter{dv_terms, x, ld_x, K, nullptr, d_a},
+                                LoraOuter{v_terms, dout, ld_dout, N, scales, d_b}, s);
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_lora_backward");
 }
 

@@ -73,10 +73,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool i
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0));
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0));
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait()
@@ -96,6 +92,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// 16 TMEM lanes x 32 FP32 columns (.16x256b four times): lane t receives, for
+// repetition i, r[4 i], r[4 i + 1] = row t / 4, columns 8 i + 2 (t % 4) and + 1,
+// and r[4 i + 2], r[4 i + 3] the same of row t / 4 + 8.
+__device__ __forceinline__ void tmem_ld16x256_x4(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
@@ -190,6 +201,41 @@ __device__ __forceinline__ Tile find_tile(const LoraRows& rows, int bt, int64_t 
     return t.find(tile);
 }
 
+// The three BF16 terms of FP32 rows [T, R], as the gradient product reads
+// them: [3][T][R8], R8 = R rounded up to 8, zeros past R.
+struct Terms {
+    uint16_t* at;  // null: not wanted
+    int64_t plane;
+    int R8;
+
+    __device__ __forceinline__ void put4(int64_t p, int r, float a, float b, float c, float d) const
+    {
+        uint2 h, m, l;
+        split3_pair(a, b, h.x, m.x, l.x);
+        split3_pair(c, d, h.y, m.y, l.y);
+        uint16_t* q = at + p * R8 + r;
+        *reinterpret_cast<uint2*>(q) = h;
+        *reinterpret_cast<uint2*>(q + plane) = m;
+        *reinterpret_cast<uint2*>(q + 2 * plane) = l;
+    }
+};
+
+// Splits rows p_lo .. p_hi - 1 of src [T, R]; threads tid of n.
+__device__ __forceinline__ void split_rows(const float* __restrict__ src, int R, const Terms& t, int p_lo, int p_hi,
+                                           int tid, int n)
+{
+    const int quads = t.R8 / 4;
+    for (int e = tid; e < (p_hi - p_lo) * quads; e += n) {
+        const int64_t p = p_lo + e / quads;
+        const int r = e % quads * 4;
+        const float* s = src + p * R + r;
+        float a[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) a[u] = r + u < R ? __ldg(s + u) : 0.0f;
+        t.put4(p, r, a[0], a[1], a[2], a[3]);
+    }
+}
+
 // Tiles of bt tokens that T tokens over n adapters can need at most.
 int64_t max_tiles(int64_t T, int n, int bt) { return ceil_div64(T, bt) + (T < n ? T : n); }
 
@@ -209,7 +255,7 @@ template <int MR>
 __global__ void __launch_bounds__(kShrinkThreads)
     lora_shrink_kernel(LoraRows rows, const uint16_t* __restrict__ x, int64_t ldx, int C,
                        const uint16_t* __restrict__ w, int R, int rblocks, const float* __restrict__ scales,
-                       float* __restrict__ v)
+                       float* __restrict__ v, Terms terms, const float* __restrict__ u, Terms u_terms)
 {
     __shared__ float red[kShrinkThreads / 32][MR * 16 * kShrinkTokens];
     __shared__ float part[MR * 16 * kShrinkTokens];
@@ -286,12 +332,26 @@ __global__ void __launch_bounds__(kShrinkThreads)
     }
     cluster.sync();
     const float f = scales ? __ldg(scales + tile.a) : 1.0f;
-    for (int e = rank * kShrinkThreads + threadIdx.x; e < kElems; e += nc * kShrinkThreads) {
-        float s = 0.0f;
-        for (int b = 0; b < nc; ++b) s += cluster.map_shared_rank(part, b)[e];
-        const int tk = e % kShrinkTokens, r = r0 + e / kShrinkTokens;
-        if (tk < tile.count && r < R) v[static_cast<int64_t>(tile.p0 + tk) * R + r] = f * s;
+    // four ranks of a token at a time
+    for (int e = rank * kShrinkThreads + threadIdx.x; e < kElems / 4; e += nc * kShrinkThreads) {
+        const int tk = e % kShrinkTokens, r4 = e / kShrinkTokens * 4, r = r0 + r4;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int b = 0; b < nc; ++b) {
+            const float* q = cluster.map_shared_rank(part, b) + r4 * kShrinkTokens + tk;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] += q[i * kShrinkTokens];
+        }
+        if (tk >= tile.count) continue;
+        const int64_t p = tile.p0 + tk;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i] = r + i < R ? f * s[i] : 0.0f;
+            if (r + i < R) v[p * R + r + i] = s[i];
+        }
+        if (terms.at && r < terms.R8) terms.put4(p, r, s[0], s[1], s[2], s[3]);
     }
+    if (u_terms.at && r0 == 0 && rank == 0)
+        split_rows(u, R, u_terms, tile.p0, tile.p0 + tile.count, threadIdx.x, kShrinkThreads);
     cluster.sync();  // the peers have read this block's part
 }
 
@@ -321,14 +381,25 @@ constexpr int tile_smem(int RP) { return 1024 + tile_stages(RP) * tile_stage_byt
 constexpr uint32_t tile_acc(int RP) { return RP <= 32 ? 32 : RP; }  // TMEM columns of one accumulator
 constexpr uint32_t tile_tmem(int RP) { return 2 * tile_acc(RP); }
 
+// Issued by one elected lane; the whole warp calls them, so that descriptors
+// and addresses stay in uniform registers.
 __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_warp(uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
 
@@ -366,7 +437,8 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc_at(uint32_t smem_addr, int
 template <int RP>
 __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
     lora_shrink_tile_kernel(const __grid_constant__ CUtensorMap wmap, LoraRows rows, const uint16_t* __restrict__ x,
-                            int64_t ldx, int C, int R, const float* __restrict__ scales, float* __restrict__ v)
+                            int64_t ldx, int C, int R, const float* __restrict__ scales, float* __restrict__ v,
+                            Terms terms, const float* __restrict__ u, Terms u_terms)
 {
     constexpr int S = tile_stages(RP);
     constexpr int kStage = tile_stage_bytes(RP);
@@ -464,9 +536,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
         cp_async_wait_all();
     } else {
         constexpr uint32_t idesc = idesc_bf16_f32(kTileTokens, RP, 0, 0);
-        // one thread runs the whole loop: votes and per-step index arithmetic
-        // would pace a stage's four MMAs
-        if (lane == 0) {
+        {
             const uint64_t da0 = sm100::sw128_kmajor_desc(ring_s);
             const uint64_t db0 = sm100::sw128_kmajor_desc(ring_s + kTileTokens * 128);
             int st = 0, turn = 0, step = 0, c = 0;
@@ -481,9 +551,9 @@ __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
                 mma_f16_ss(d, da + 2, db + 2, idesc, 1u);
                 mma_f16_ss(d, da + 4, db + 4, idesc, 1u);
                 mma_f16_ss(d, da + 6, db + 6, idesc, 1u);
-                sm100::mma_commit(sm100::smem_u32(&s_empty[st]));
+                mma_commit_warp(sm100::smem_u32(&s_empty[st]));
                 if (++step == kTileChain || i == mine - 1) {
-                    sm100::mma_commit(sm100::smem_u32(&s_ready[c & 1]));
+                    mma_commit_warp(sm100::smem_u32(&s_ready[c & 1]));
                     step = 0;
                     ++c;
                 }
@@ -523,16 +593,25 @@ __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
             s.z += t.z;
             s.w += t.w;
         }
-        float* const d = v + static_cast<int64_t>(tile.p0 + row) * R + r;
+        s = make_float4(f * s.x, r + 1 < R ? f * s.y : 0.0f, r + 2 < R ? f * s.z : 0.0f, r + 3 < R ? f * s.w : 0.0f);
+        const int64_t p = tile.p0 + row;
+        float* const d = v + p * R + r;
         if (R % 4 == 0) {
-            *reinterpret_cast<float4*>(d) = make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
+            *reinterpret_cast<float4*>(d) = s;
         } else {
-            d[0] = f * s.x;
-            if (r + 1 < R) d[1] = f * s.y;
-            if (r + 2 < R) d[2] = f * s.z;
-            if (r + 3 < R) d[3] = f * s.w;
+            d[0] = s.x;
+            if (r + 1 < R) d[1] = s.y;
+            if (r + 2 < R) d[2] = s.z;
+            if (r + 3 < R) d[3] = s.w;
+        }
+        if (terms.at) {
+            terms.put4(p, r, s.x, s.y, s.z, s.w);
+            if (r + 4 >= R && r + 4 < terms.R8) terms.put4(p, r + 4, 0.0f, 0.0f, 0.0f, 0.0f);
         }
     }
+    if (u_terms.at)
+        split_rows(u, R, u_terms, tile.p0 + min(rank * per, tile.count), tile.p0 + min((rank + 1) * per, tile.count), tid,
+                   kTileThreads);
     cluster.sync();  // the peers have read this block's sums
 }
 
@@ -896,7 +975,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     alive = alive && wait(bar(kSlabIn, sl), u >> 1);
                     alive = __all_sync(0xFFFFFFFFu, alive);
                     if (!alive) break;
-                    if (lane == 0) {
+                    {
                         sm100::tc_fence_after();
                         const uint64_t dw = sw128_mnmajor_desc(sm100::smem_u32(slabs + sl * kSlab), RP * 128);
 #pragma unroll
@@ -906,8 +985,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                 const uint64_t dv = sw128_kmajor_desc_at(sm100::smem_u32(mem), sp * RP + k * 16);
                                 mma_f16_ss(tmem + d * W, dv, dw + k * 2048 / 16, idesc, (sp != 2 || k != 0) ? 1u : 0u);
                             }
-                        sm100::mma_commit(bar(kReady, d));
-                        sm100::mma_commit(bar(kSlabUsed, sl));
+                        mma_commit_warp(bar(kReady, d));
+                        mma_commit_warp(bar(kSlabUsed, sl));
                     }
                     __syncwarp();
                     if (j > 0) {  // the slab before is free: fetch the one after this
@@ -994,55 +1073,92 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
 // ------------------------------------------------------------------- outer
 //
-// d[a, r, c] = f_a sum_p v[p, r] x[tok, c], 64 ranks times 128 columns per
-// cluster on tcgen05; tokens are the K of the product, dealt in equal runs to
-// the cluster's blocks.  Both operands lie in shared memory token by token,
-// 64 values (128 bytes, 128-byte swizzle) per token and panel, so they are
-// MN-major.  Four producer warps bring in the x rows (gathered) and the raw
-// rows of v by cp.async; four more split v into its three terms, and move the
-// accumulator to FP32 registers every kOuterChain stages (two TMEM buffers in
-// turn), so no long sum is left to the tensor core's rounding; one thread
-// issues the MMAs, three per 16 tokens into one accumulator.  Two blocks per
-// SM cover each other's start and end.  The blocks' sums are joined in block
-// order.
+// d[a, r, c] = f_a sum_p v[p, r] x[tok, c], an item being 64 ranks times 128
+// columns of one adapter, on tcgen05 with the tokens as the K of the product.
+// Both operands lie in shared memory token by token, 64 values (128 bytes,
+// 128-byte swizzle) per token and panel, so they are MN-major: x comes in by
+// cp.async (gathered rows), the three terms of v, which the shrink before left
+// split, by TMA (by cp.async in an item's last stage, whose rows past the
+// adapter's tokens have to be zeros).  One thread issues the MMAs, three per
+// 16 tokens into one accumulator; four warps move it to FP32 registers every
+// kOuterChain stages (two TMEM buffers in turn), so no long sum is left to the
+// tensor core's rounding, and write an item out.  Blocks are persistent, two
+// per SM, and the ring runs on from item to item: an item is a few stages,
+// shorter than a block's start and end (one item per block: 149 us for the
+// whole GLM-sized gradient against %OUTER%).  With few adapters there are too few
+// items for that; then the blocks of a cluster share one item's tokens and
+// join their sums in block order.
 constexpr int kOuterThreads = 288;
 constexpr int kOuterRanks = 64;
 constexpr int kOuterCols = 128;
 constexpr int kOuterTokens = 32;   // per stage
-constexpr int kOuterStages = 3;
+constexpr int kOuterStages = 5;
 constexpr int kOuterChain = 4;
 constexpr int kOuterPanel = kOuterTokens * 128;
-constexpr int kOuterRawPitch = kOuterRanks * 4 + 16;  // bytes
-constexpr int kOuterX = 0, kOuterV = (kOuterCols / 64) * kOuterPanel, kOuterRaw = kOuterV + 3 * kOuterPanel;
-constexpr int kOuterStageBytes = (kOuterRaw + kOuterTokens * kOuterRawPitch + 1023) / 1024 * 1024;
+constexpr int kOuterV = (kOuterCols / 64) * kOuterPanel;  // panels of x, then three of v
+constexpr int kOuterStageBytes = kOuterV + 3 * kOuterPanel;
 constexpr int kOuterPitch = kOuterCols + 4;  // floats per rank row of the block's sums
 constexpr int kOuterSmem = 1024 + kOuterStages * kOuterStageBytes;
 static_assert(kOuterRanks * kOuterPitch * 4 <= kOuterStages * kOuterStageBytes, "the sums reuse the ring");
 
+// One of the two products, its terms of v and where they lie.
+struct OuterSide {
+    Terms v;
+    const uint16_t* x;
+    int64_t ldx;
+    int C;
+    const float* scales;
+    float* d;
+};
+
+// The item's part of the problem: which product, adapter, ranks and columns,
+// and this block's run of the adapter's tokens in whole stages.
+struct OuterItem {
+    bool first;
+    int a, r0, c0, C;
+    int p0, hi, stages;
+};
+__device__ __forceinline__ OuterItem outer_item(const LoraRows& rows, int64_t item, int ablocks, int blocks, int rblocks,
+                                                int Ca, int Cb, int rank, int nc)
+{
+    OuterItem o;
+    const int blk = static_cast<int>(item % blocks);
+    const int ar = static_cast<int>(item / blocks);
+    o.first = blk < ablocks;
+    o.C = o.first ? Ca : Cb;
+    o.c0 = (o.first ? blk : blk - ablocks) * kOuterCols;
+    o.a = ar / rblocks;
+    o.r0 = ar % rblocks * kOuterRanks;
+    const int T = static_cast<int>(rows.T);
+    const int lo = min(max(__ldg(rows.offsets + o.a), 0), T);
+    o.hi = min(max(__ldg(rows.offsets + o.a + 1), lo), T);
+    const int all = (o.hi - lo + kOuterTokens - 1) / kOuterTokens;
+    const int s_lo = static_cast<int>(static_cast<int64_t>(all) * rank / nc);
+    o.stages = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / nc) - s_lo;
+    o.p0 = lo + s_lo * kOuterTokens;
+    return o;
+}
+
 __global__ void __launch_bounds__(kOuterThreads, 2)
-    lora_outer_kernel(LoraRows rows, int R, int rblocks, LoraOuter pa, LoraOuter pb, int ablocks)
+    lora_outer_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                      LoraRows rows, int R, int rblocks, OuterSide pa, OuterSide pb, int ablocks, int blocks)
 {
     constexpr int S = kOuterStages;
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t s_full[S], s_split[S], s_empty[S], s_ready[2], s_read[2];
+    __shared__ __align__(8) uint64_t s_full[S], s_empty[S], s_ready[2], s_read[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = static_cast<int>(cluster.num_blocks());
     const int rank = static_cast<int>(cluster.block_rank());
-    const int blk = static_cast<int>(blockIdx.x) / nc;
-    const bool first = blk < ablocks;
-    const int C = first ? pa.C : pb.C;
-    const int c0 = (first ? blk : blk - ablocks) * kOuterCols;
-    const int a = blockIdx.y / rblocks;
-    const int r0 = (blockIdx.y % rblocks) * kOuterRanks;
+    const int64_t items = static_cast<int64_t>(blocks) * rblocks * rows.n;
+    const int64_t item0 = blockIdx.x / nc, step_items = gridDim.x / nc;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
     const uint32_t ring_s = sm100::smem_u32(ring);
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            sm100::mbar_init(sm100::smem_u32(&s_full[i]), 128);
-            sm100::mbar_init(sm100::smem_u32(&s_split[i]), 128);
+            sm100::mbar_init(sm100::smem_u32(&s_full[i]), 128 + 1);  // the copies of x, the terms of v
             sm100::mbar_init(sm100::smem_u32(&s_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -1060,183 +1176,198 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
     __syncthreads();
     sm100::tc_fence_after();
     const uint32_t tmem = s_tmem;
-    // this block's run of the adapter's tokens, in whole stages
-    const int T = static_cast<int>(rows.T);
-    const int lo = min(max(__ldg(rows.offsets + a), 0), T);
-    const int hi = min(max(__ldg(rows.offsets + a + 1), lo), T);
-    const int stages = (hi - lo + kOuterTokens - 1) / kOuterTokens;
-    const int s_lo = static_cast<int>(static_cast<int64_t>(stages) * rank / nc);
-    const int mine = static_cast<int>(static_cast<int64_t>(stages) * (rank + 1) / nc) - s_lo;
-    const int p0 = lo + s_lo * kOuterTokens;
     auto wait = [&](uint64_t* b, int phase) {
         return sm100::mbar_wait_bounded(sm100::smem_u32(b), phase & 1, &s_abort, kTileWaitNs);
     };
-    wait_previous();  // dv
-    float sum[kOuterCols / 64][32];
+    auto item_at = [&](int64_t item) {
+        return outer_item(rows, item, ablocks, blocks, rblocks, pa.C, pb.C, rank, nc);
+    };
+    float sum[kOuterCols / 32][16];
     if (warp < 4) {
-        // v: token vt, ranks vr .. vr + 15 of the block's 64
-        const int vt = tid >> 2, vr = (tid & 3) * 16;
+        int c = 0;  // chains so far
+        bool ok = true;
+        for (int64_t item = item0; item < items; item += step_items) {
+            const OuterItem o = item_at(item);
 #pragma unroll
-        for (int j = 0; j < kOuterCols / 64; ++j)
+            for (int j = 0; j < kOuterCols / 32; ++j)
 #pragma unroll
-            for (int u = 0; u < 32; ++u) sum[j][u] = 0.0f;
-        auto promote = [&](int c) {
-            if (!wait(&s_ready[c & 1], c >> 1)) return;
-            __syncwarp();
-            sm100::tc_fence_after();
+                for (int u = 0; u < 16; ++u) sum[j][u] = 0.0f;
+            for (int i = 0; i < o.stages; i += kOuterChain, ++c) {
+                ok = ok && wait(&s_ready[c & 1], c >> 1);
+                if (!ok) break;
+                __syncwarp();
+                sm100::tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < kOuterCols / 64; ++j) {
-                uint32_t t[32];
-                sm100::tmem_ld16x256_x8_issue(
-                    tmem + (static_cast<uint32_t>(warp) << 21) + (c & 1) * kOuterCols + j * 64, t);
-                sm100::tmem_ld_wait(t);
+                for (int j = 0; j < kOuterCols / 32; ++j) {
+                    uint32_t t[16];
+                    tmem_ld16x256_x4(tmem + (static_cast<uint32_t>(warp) << 21) + (c & 1) * kOuterCols + j * 32, t);
 #pragma unroll
-                for (int u = 0; u < 32; ++u) sum[j][u] += __uint_as_float(t[u]);
+                    for (int u = 0; u < 16; ++u) sum[j][u] += __uint_as_float(t[u]);
+                }
+                sm100::tc_fence_before();
+                sm100::mbar_arrive(sm100::smem_u32(&s_read[c & 1]));
             }
-            sm100::tc_fence_before();
-            sm100::mbar_arrive(sm100::smem_u32(&s_read[c & 1]));
-        };
-        int done = 0;  // chains in registers
-        for (int i = 0; i < mine; ++i) {
-            // the stage's MMAs of S stages ago are complete (its raw rows too
-            // are only there since), and with them a chain that ended there
-            if (!wait(&s_full[i % S], i / S)) break;
-            if (i >= S && (i - S + 1) % kOuterChain == 0) promote(done++);
-            uint8_t* const st = ring + (i % S) * kOuterStageBytes;
-            const float4* raw = reinterpret_cast<const float4*>(st + kOuterRaw + vt * kOuterRawPitch + vr * 4);
-            uint8_t* const dst = st + kOuterV + vt * 128;
+            if (nc > 1) break;  // one item per cluster: joined below
+            // lane l holds ranks 16 warp + l / 4 (+ 8), columns 32 j + 8 i +
+            // 2 (l % 4) and + 1; a wait that ran out leaves NaN
+            const float* const scales = o.first ? pa.scales : pb.scales;
+            const float f = !ok ? NAN : scales ? __ldg(scales + o.a) : 1.0f;
+            float* const d = (o.first ? pa.d : pb.d) + (static_cast<int64_t>(o.a) * R + o.r0) * o.C + o.c0;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float4 p = raw[2 * u], q = raw[2 * u + 1];
-                uint4 h, m, l;
-                split3_pair(p.x, p.y, h.x, m.x, l.x);
-                split3_pair(p.z, p.w, h.y, m.y, l.y);
-                split3_pair(q.x, q.y, h.z, m.z, l.z);
-                split3_pair(q.z, q.w, h.w, m.w, l.w);
-                const int at = ((vr / 8 + u) ^ (vt & 7)) << 4;
-                *reinterpret_cast<uint4*>(dst + at) = h;
-                *reinterpret_cast<uint4*>(dst + kOuterPanel + at) = m;
-                *reinterpret_cast<uint4*>(dst + 2 * kOuterPanel + at) = l;
+            for (int h = 0; h < 2; ++h) {
+                const int row = 16 * warp + lane / 4 + 8 * h;
+                if (o.r0 + row >= R) continue;
+#pragma unroll
+                for (int j = 0; j < kOuterCols / 32; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int col = 32 * j + 8 * i + 2 * (lane % 4);
+                        if (o.c0 + col < o.C)
+                            *reinterpret_cast<float2*>(d + static_cast<int64_t>(row) * o.C + col) =
+                                make_float2(f * sum[j][4 * i + 2 * h], f * sum[j][4 * i + 2 * h + 1]);
+                    }
             }
-            sm100::fence_proxy_async_smem();
-            sm100::mbar_arrive(sm100::smem_u32(&s_split[i % S]));
         }
-        const int chains = (mine + kOuterChain - 1) / kOuterChain;
-        while (done < chains && !*static_cast<volatile int*>(&s_abort)) promote(done++);
     } else if (warp < 8) {
-        const float* const pv = first ? pa.v : pb.v;
-        const uint16_t* const px = first ? pa.x : pb.x;
-        const int64_t ldx = first ? pa.ldx : pb.ldx;
         const int pt = tid - 128;
-        // x: piece ch (8 columns) of the panels, token rows row0 and row0 + 16
+        // piece ch (8 values) of the panels, token rows row0 and row0 + 16
         const int ch = pt & 7, row0 = pt >> 3;
         const uint32_t swz = static_cast<uint32_t>(ch ^ (row0 & 7)) << 4;
-        // v: ranks r4 .. r4 + 3 of token rows v0 + 8 h
-        const int r4 = (pt & 15) * 4, v0 = pt >> 4;
-        int next[kOuterTokens / 16];  // token rows of the next stage
-        auto load_tokens = [&](int i) {
+        const int T = static_cast<int>(rows.T);
+        int st = 0, turn = 0;
+        bool ok = true, waited = false;
+        for (int64_t item = item0; item < items && ok; item += step_items) {
+            const OuterItem o = item_at(item);
+            const uint16_t* const px = o.first ? pa.x : pb.x;
+            const int64_t ldx = o.first ? pa.ldx : pb.ldx;
+            const Terms pv = o.first ? pa.v : pb.v;
+            int next[2];  // token rows of the next stage
+            auto load_tokens = [&](int i) {
 #pragma unroll
-            for (int h = 0; h < kOuterTokens / 16; ++h) {
-                const int at = p0 + i * kOuterTokens + row0 + 16 * h;
-                next[h] = at < hi ? __ldg(rows.tokens + at) : -1;
-            }
-        };
-        load_tokens(0);
-        for (int i = 0; i < mine; ++i) {
-            int cur[kOuterTokens / 16];
-#pragma unroll
-            for (int h = 0; h < kOuterTokens / 16; ++h) cur[h] = next[h];
-            load_tokens(i + 1);
-            if (i >= S && !wait(&s_empty[i % S], i / S - 1)) break;
-            const uint32_t st = ring_s + (i % S) * kOuterStageBytes;
-            const int p = p0 + i * kOuterTokens;
-#pragma unroll
-            for (int h = 0; h < kOuterTokens / 16; ++h) {
-                const int tok = cur[h];
-                const bool row = tok >= 0 && tok < T;
-                const uint16_t* src = px + (row ? tok * ldx : 0) + c0 + ch * 8;
-#pragma unroll
-                for (int j = 0; j < kOuterCols / 64; ++j) {
-                    const bool ok = row && c0 + j * 64 + ch * 8 < C;
-                    cp_async16(st + kOuterX + j * kOuterPanel + (row0 + 16 * h) * 128 + swz, ok ? src + j * 64 : px, ok);
+                for (int h = 0; h < 2; ++h) {
+                    const int at = o.p0 + i * kOuterTokens + row0 + 16 * h;
+                    next[h] = at < o.hi ? __ldg(rows.tokens + at) : -1;
                 }
-            }
+            };
+            load_tokens(0);
+            for (int i = 0; i < o.stages; ++i) {
+                const int cur[2] = {next[0], next[1]};
+                load_tokens(i + 1);
+                ok = ok && (turn == 0 || wait(&s_empty[st], turn - 1));
+                if (!ok) break;
+                const uint32_t at = ring_s + st * kOuterStageBytes;
+                const uint32_t bar = sm100::smem_u32(&s_full[st]);
+                const int p = o.p0 + i * kOuterTokens;
 #pragma unroll
-            for (int h = 0; h < kOuterTokens / 8; ++h) {
-                const int row = v0 + 8 * h;
-                const uint32_t dst = st + kOuterRaw + row * kOuterRawPitch + r4 * 4;
-                const float* src = pv + static_cast<int64_t>(p + row) * R + r0 + r4;
-                if (R % 4 == 0) {
-                    const bool ok = p + row < hi && r0 + r4 < R;
-                    cp_async16(dst, ok ? src : pv, ok);
-                } else {
+                for (int h = 0; h < 2; ++h) {
+                    const bool row = cur[h] >= 0 && cur[h] < T;
+                    const uint16_t* src = px + (row ? cur[h] * ldx : 0) + o.c0 + ch * 8;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const bool ok = p + row < hi && r0 + r4 + u < R;
-                        cp_async4(dst + 4 * u, ok ? src + u : pv, ok);
+                    for (int j = 0; j < kOuterCols / 64; ++j) {
+                        const bool in = row && o.c0 + j * 64 + ch * 8 < o.C;
+                        cp_async16(at + j * kOuterPanel + (row0 + 16 * h) * 128 + swz, in ? src + j * 64 : px, in);
                     }
                 }
+                if (!waited) wait_previous();  // the terms of dv
+                waited = true;
+                if (p + kOuterTokens <= o.hi) {
+                    if (pt == 0) {
+                        sm100::mbar_arrive_expect_tx(bar, 3 * kOuterPanel);
+                        for (int sp = 0; sp < 3; ++sp)
+                            sm100::tma_load_3d(at + kOuterV + sp * kOuterPanel, o.first ? &map_a : &map_b, o.r0 * 2, p,
+                                               sp, bar);
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int sp = 0; sp < 3; ++sp) {
+                            const int row = p + row0 + 16 * h;
+                            const bool in = row < o.hi && o.r0 + ch * 8 < pv.R8;
+                            cp_async16(
+                                at + kOuterV + sp * kOuterPanel + (row0 + 16 * h) * 128 + swz,
+                                in ? pv.at + sp * pv.plane + static_cast<int64_t>(row) * pv.R8 + o.r0 + ch * 8 : pv.at,
+                                in);
+                        }
+                    if (pt == 0) sm100::mbar_arrive(bar);
+                }
+                cp_async_arrive(bar);
+                if (++st == S) {
+                    st = 0;
+                    ++turn;
+                }
             }
-            cp_async_arrive(sm100::smem_u32(&s_full[i % S]));
         }
         cp_async_wait_all();
     } else {
         constexpr uint32_t idesc = idesc_bf16_f32(kOuterRanks, kOuterCols, 1, 1);
-        for (int i = 0; i < mine; ++i) {
-            const int c = i / kOuterChain;
-            bool ok = true;
-            if (i % kOuterChain == 0 && c >= 2) ok = wait(&s_read[c & 1], (c >> 1) - 1);
-            ok = ok && wait(&s_full[i % S], i / S) && wait(&s_split[i % S], i / S);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            if (lane == 0) {
+        const uint64_t dx0 = sw128_mnmajor_desc(ring_s, kOuterPanel);
+        const uint64_t dv0 = sw128_mnmajor_desc(ring_s + kOuterV, kOuterPanel);
+        int st = 0, turn = 0, c = 0;
+        bool ok = true;
+        for (int64_t item = item0; item < items && ok; item += step_items) {
+            const OuterItem o = item_at(item);
+            int step = 0;
+            for (int i = 0; i < o.stages; ++i) {
+                if (step == 0 && c >= 2) ok = ok && wait(&s_read[c & 1], (c >> 1) - 1);
+                ok = ok && wait(&s_full[st], turn);
+                if (!ok) break;
                 sm100::fence_proxy_async_smem();
                 sm100::tc_fence_after();
-                const uint32_t st = ring_s + (i % S) * kOuterStageBytes;
-                const uint64_t dx = sw128_mnmajor_desc(st + kOuterX, kOuterPanel);
-                const uint64_t dv = sw128_mnmajor_desc(st + kOuterV, kOuterPanel);
+                const uint64_t dx = dx0 + st * (kOuterStageBytes / 16), dv = dv0 + st * (kOuterStageBytes / 16);
+                const uint32_t d = tmem + (c & 1) * kOuterCols;
 #pragma unroll
                 for (int kk = 0; kk < kOuterTokens / 16; ++kk)
 #pragma unroll
                     for (int sp = 2; sp >= 0; --sp)  // 16 token rows are 2048 bytes
-                        mma_f16_ss(tmem + (c & 1) * kOuterCols, dv + (sp * kOuterPanel + kk * 2048) / 16,
-                                   dx + kk * 2048 / 16, idesc,
-                                   (i % kOuterChain != 0 || kk != 0 || sp != 2) ? 1u : 0u);
-                sm100::mma_commit(sm100::smem_u32(&s_empty[i % S]));
-                if (i % kOuterChain == kOuterChain - 1 || i == mine - 1)
-                    sm100::mma_commit(sm100::smem_u32(&s_ready[c & 1]));
+                        mma_f16_ss(d, dv + (sp * kOuterPanel + kk * 2048) / 16, dx + kk * 2048 / 16, idesc,
+                                   (step != 0 || kk != 0 || sp != 2) ? 1u : 0u);
+                mma_commit_warp(sm100::smem_u32(&s_empty[st]));
+                if (++step == kOuterChain || i == o.stages - 1) {
+                    mma_commit_warp(sm100::smem_u32(&s_ready[c & 1]));
+                    step = 0;
+                    ++c;
+                }
+                if (++st == S) {
+                    st = 0;
+                    ++turn;
+                }
             }
-            __syncwarp();
         }
     }
+    __syncwarp();
     __syncthreads();  // every chain is read: the MMAs and the ring are done with
+    wait_previous();  // (blocks without a stage) never end before the kernel they follow
     if (warp == 8) {
         sm100::tc_fence_after();
         sm100::tmem_dealloc(tmem, 2 * kOuterCols);
     }
-    // the block's sums: lane l holds ranks 16 warp + l / 4 (+ 8), columns
-    // 64 j + 8 i + 2 (l % 4) and + 1; a wait that ran out leaves NaN
+    if (nc == 1) return;
+    // a cluster's sums
+    const OuterItem o = item_at(item0);
     float* const part = reinterpret_cast<float*>(ring);
     if (warp < 4) {
         const bool bad = s_abort != 0;
 #pragma unroll
-        for (int j = 0; j < kOuterCols / 64; ++j)
+        for (int j = 0; j < kOuterCols / 32; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<float2*>(part + (16 * warp + lane / 4 + 8 * h) * kOuterPitch + 64 * j + 8 * i +
+                    *reinterpret_cast<float2*>(part + (16 * warp + lane / 4 + 8 * h) * kOuterPitch + 32 * j + 8 * i +
                                                2 * (lane % 4)) =
                         bad ? make_float2(NAN, NAN)
                             : make_float2(sum[j][4 * i + 2 * h], sum[j][4 * i + 2 * h + 1]);
     }
     cluster.sync();
-    const float* const scales = first ? pa.scales : pb.scales;
-    const float f = scales ? __ldg(scales + a) : 1.0f;
-    float* const d = (first ? pa.d : pb.d) + static_cast<int64_t>(a) * R * C;
+    const float* const scales = o.first ? pa.scales : pb.scales;
+    const float f = scales ? __ldg(scales + o.a) : 1.0f;
+    float* const d = (o.first ? pa.d : pb.d) + (static_cast<int64_t>(o.a) * R + o.r0) * o.C + o.c0;
     const int per = kOuterRanks / nc;  // this block's rank rows
+#pragma unroll 4
     for (int e = tid; e < per * (kOuterCols / 4); e += kOuterThreads) {
         const int row = rank * per + e / (kOuterCols / 4), c = e % (kOuterCols / 4) * 4;
-        if (r0 + row >= R || c0 + c >= C) continue;
+        if (o.r0 + row >= R || o.c0 + c >= o.C) continue;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int b = 0; b < nc; ++b) {
             const float4 t = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, b) + row * kOuterPitch + c);
@@ -1245,7 +1376,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
             s.z += t.z;
             s.w += t.w;
         }
-        *reinterpret_cast<float4*>(d + static_cast<int64_t>(r0 + row) * C + c0 + c) =
+        *reinterpret_cast<float4*>(d + static_cast<int64_t>(row) * o.C + c) =
             make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
     }
     cluster.sync();  // the peers have read this block's sums
@@ -1305,18 +1436,20 @@ bool rank_map(CUtensorMap* map, const LoraRows& rows, const uint16_t* w, int R, 
 
 template <int MR>
 cudaError_t shrink(const LoraRows& rows, const uint16_t* x, int64_t ldx, int C, const uint16_t* w, int R,
-                   const float* scales, float* v, int sm_count, cudaStream_t s)
+                   const float* scales, float* v, const Terms& t, const float* u, const Terms& ut, int sm_count,
+                   cudaStream_t s)
 {
     const int rblocks = (R + 16 * MR - 1) / (16 * MR);
     const int64_t units = max_tiles(rows.T, rows.n, kShrinkTokens) * rblocks;
     const int nc = cluster_size(units, (C + 31) / 32, 2 * (kShrinkThreads / 32), sm_count);
     Launch l(units * nc, kShrinkThreads, 0, s, nc, false);
-    return cudaLaunchKernelEx(&l.cfg, lora_shrink_kernel<MR>, rows, x, ldx, C, w, R, rblocks, scales, v);
+    return cudaLaunchKernelEx(&l.cfg, lora_shrink_kernel<MR>, rows, x, ldx, C, w, R, rblocks, scales, v, t, u, ut);
 }
 
 template <int RP>
 cudaError_t shrink_tile(const LoraRows& rows, const uint16_t* x, int64_t ldx, int C, const uint16_t* w, int R,
-                        const float* scales, float* v, int sm_count, cudaStream_t s)
+                        const float* scales, float* v, const Terms& t, const float* u, const Terms& ut, int sm_count,
+                        cudaStream_t s)
 {
     const int64_t units = max_tiles(rows.T, rows.n, kTileTokens);
     const int nc = cluster_size(units, (C + 63) / 64, 4, sm_count);
@@ -1325,7 +1458,7 @@ cudaError_t shrink_tile(const LoraRows& rows, const uint16_t* x, int64_t ldx, in
     cudaError_t err = allow_smem(lora_shrink_tile_kernel<RP>, tile_smem(RP));
     if (err != cudaSuccess) return err;
     Launch l(units * nc, kTileThreads, tile_smem(RP), s, nc, false);
-    return cudaLaunchKernelEx(&l.cfg, lora_shrink_tile_kernel<RP>, map, rows, x, ldx, C, R, scales, v);
+    return cudaLaunchKernelEx(&l.cfg, lora_shrink_tile_kernel<RP>, map, rows, x, ldx, C, R, scales, v, t, u, ut);
 }
 
 template <int RP>
@@ -1356,22 +1489,31 @@ cudaError_t expand(const LoraRows& rows, const float* v, int R, const uint16_t* 
                               out, ld_out, out_bf16);
 }
 
+int round8(int R) { return (R + 7) / 8 * 8; }
+
+Terms terms_at(uint16_t* at, int64_t T, int R) { return Terms{at, T * round8(R), round8(R)}; }
+
 }  // namespace
 
+size_t lora_terms_bytes(int64_t T, int R) { return static_cast<size_t>(T) * round8(R) * 3 * 2; }
+
 cudaError_t launch_lora_shrink(const LoraRows& rows, const uint16_t* x, int64_t ldx, int C, const uint16_t* w, int R,
-                               const float* scales, float* v, cudaStream_t s)
+                               const float* scales, float* v, uint16_t* v_terms, const float* u, uint16_t* u_terms,
+                               cudaStream_t s)
 {
     DeviceInfo di;
     if (!device_info(&di)) return cudaErrorUnknown;
+    const Terms t = terms_at(v_terms, rows.T, R), ut = terms_at(u_terms, rows.T, R);
+    const int sms = di.sm_count;
     if (rows.T >= 256 && rows.T >= 16 * static_cast<int64_t>(rows.n)) {
-        if (R <= 16) return shrink_tile<16>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
-        if (R <= 32) return shrink_tile<32>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
-        if (R <= 64) return shrink_tile<64>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
-        return shrink_tile<128>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
+        if (R <= 16) return shrink_tile<16>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
+        if (R <= 32) return shrink_tile<32>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
+        if (R <= 64) return shrink_tile<64>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
+        return shrink_tile<128>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
     }
-    if (R <= 16) return shrink<1>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
-    if (R <= 32) return shrink<2>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
-    return shrink<4>(rows, x, ldx, C, w, R, scales, v, di.sm_count, s);
+    if (R <= 16) return shrink<1>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
+    if (R <= 32) return shrink<2>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
+    return shrink<4>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
 }
 
 cudaError_t launch_lora_expand(const LoraRows& rows, const float* v, int R, const uint16_t* w, int C,
@@ -1399,15 +1541,29 @@ cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, c
 {
     const int rblocks = (R + kOuterRanks - 1) / kOuterRanks;
     const int ab = (a.C + kOuterCols - 1) / kOuterCols, bb = (b.C + kOuterCols - 1) / kOuterCols;
-    // blocks per cluster (they share an adapter's tokens): about 128 tokens
-    // each, so that an adapter with many tokens does not outlast the others
+    DeviceInfo di;
+    if (!device_info(&di)) return cudaErrorUnknown;
+    // persistent blocks where there are two items for each; else clusters that
+    // share an item's tokens, as many blocks as the GPU holds
+    const int64_t items = static_cast<int64_t>(ab + bb) * rblocks * rows.n, resident = 2 * di.sm_count;
     int nc = 1;
-    while (nc < 8 && rows.T >= 2 * static_cast<int64_t>(nc) * rows.n * 128) nc *= 2;
+    if (items < 2 * resident)
+        while (nc < 8 && items * nc * 2 <= 2 * resident && rows.T >= 2 * static_cast<int64_t>(nc) * rows.n * 64) nc *= 2;
+    const int64_t grid = nc > 1 ? items * nc : items < resident ? items : resident;
+    OuterSide side[2];
+    CUtensorMap map[2];
+    for (int i = 0; i < 2; ++i) {
+        const LoraOuter& o = i == 0 ? a : b;
+        side[i] = OuterSide{terms_at(const_cast<uint16_t*>(o.v_terms), rows.T, R), o.x, o.ldx, o.C, o.scales, o.d};
+        const uint64_t row = static_cast<uint64_t>(side[i].v.R8) * 2, t1 = rows.T > 0 ? rows.T : 1;
+        const uint64_t dims[3] = {row, t1, 3}, strides[2] = {row, t1 * row};
+        if (!make_tmap_u8(&map[i], o.v_terms, 3, dims, strides, kOuterTokens)) return cudaErrorNotSupported;
+    }
     cudaError_t err = allow_smem(lora_outer_kernel, kOuterSmem);
     if (err != cudaSuccess) return err;
-    Launch l(static_cast<int64_t>(ab + bb) * nc, kOuterThreads, kOuterSmem, s, nc, true);
-    l.cfg.gridDim.y = static_cast<unsigned>(rows.n * rblocks);
-    return cudaLaunchKernelEx(&l.cfg, lora_outer_kernel, rows, R, rblocks, a, b, ab);
+    Launch l(grid, kOuterThreads, kOuterSmem, s, nc, true);
+    return cudaLaunchKernelEx(&l.cfg, lora_outer_kernel, map[0], map[1], rows, R, rblocks, side[0], side[1], ab,
+                              ab + bb);
 }
 
 }  // namespace fp8moe
