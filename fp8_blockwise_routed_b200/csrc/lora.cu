@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
     if (tile.a < 0) return;  // the whole cluster
     uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
     const uint32_t ring_s = sm100::smem_u32(ring);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             sm100::mbar_init(sm100::smem_u32(&s_full[i]), 128 + 1);  // the copies of x, the box of w
@@ -1085,9 +1085,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // tensor core's rounding, and write an item out.  Blocks are persistent, two
 // per SM, and the ring runs on from item to item: an item is a few stages,
 // shorter than a block's start and end (one item per block: 149 us for the
-// whole GLM-sized gradient against %OUTER%).  With few adapters there are too few
-// items for that; then the blocks of a cluster share one item's tokens and
-// join their sums in block order.
+// whole GLM-sized gradient against 111).  Items go from the adapter with most
+// tokens to the one with fewest, dealt to the blocks there and back, so that
+// uneven adapters even out.  With few adapters there are too few items for
+// that; then the blocks of a cluster share one item's tokens and join their
+// sums in block order.
 constexpr int kOuterThreads = 288;
 constexpr int kOuterRanks = 64;
 constexpr int kOuterCols = 128;
@@ -1118,8 +1120,8 @@ struct OuterItem {
     int a, r0, c0, C;
     int p0, hi, stages;
 };
-__device__ __forceinline__ OuterItem outer_item(const LoraRows& rows, int64_t item, int ablocks, int blocks, int rblocks,
-                                                int Ca, int Cb, int rank, int nc)
+__device__ __forceinline__ OuterItem outer_item(const LoraRows& rows, const int16_t* order, int64_t item, int ablocks,
+                                                int blocks, int rblocks, int Ca, int Cb, int rank, int nc)
 {
     OuterItem o;
     const int blk = static_cast<int>(item % blocks);
@@ -1127,7 +1129,7 @@ __device__ __forceinline__ OuterItem outer_item(const LoraRows& rows, int64_t it
     o.first = blk < ablocks;
     o.C = o.first ? Ca : Cb;
     o.c0 = (o.first ? blk : blk - ablocks) * kOuterCols;
-    o.a = ar / rblocks;
+    o.a = order[ar / rblocks];
     o.r0 = ar % rblocks * kOuterRanks;
     const int T = static_cast<int>(rows.T);
     const int lo = min(max(__ldg(rows.offsets + o.a), 0), T);
@@ -1148,6 +1150,8 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
     __shared__ __align__(8) uint64_t s_full[S], s_empty[S], s_ready[2], s_read[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ int s_count[kOuterThreads];
+    __shared__ int16_t s_order[1024];  // n <= 1024
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = static_cast<int>(cluster.num_blocks());
     const int rank = static_cast<int>(cluster.block_rank());
@@ -1172,6 +1176,22 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
         sm100::tmem_alloc(sm100::smem_u32(&s_tmem), 2 * kOuterCols);
         sm100::tmem_relinquish();
     }
+    // adapters by falling number of tokens; with more adapters than threads
+    // there are items enough to even out in any order
+    const bool sorted = nc == 1 && rows.n <= kOuterThreads;
+    int count = 0;
+    if (sorted && tid < rows.n) {
+        count = __ldg(rows.offsets + tid + 1) - __ldg(rows.offsets + tid);
+        s_count[tid] = count;
+    }
+    __syncthreads();
+    if (!sorted) {
+        for (int i = tid; i < rows.n; i += kOuterThreads) s_order[i] = static_cast<int16_t>(i);
+    } else if (tid < rows.n) {
+        int at = 0;
+        for (int b = 0; b < rows.n; ++b) at += s_count[b] > count || (s_count[b] == count && b < tid);
+        s_order[at] = static_cast<int16_t>(tid);
+    }
     sm100::tc_fence_before();
     __syncthreads();
     sm100::tc_fence_after();
@@ -1179,15 +1199,20 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
     auto wait = [&](uint64_t* b, int phase) {
         return sm100::mbar_wait_bounded(sm100::smem_u32(b), phase & 1, &s_abort, kTileWaitNs);
     };
+    // this block's item of a round (there in even rounds, back in odd ones)
+    auto item_of = [&](int64_t round) {
+        return round * step_items + ((round & 1) ? step_items - 1 - item0 : item0);
+    };
     auto item_at = [&](int64_t item) {
-        return outer_item(rows, item, ablocks, blocks, rblocks, pa.C, pb.C, rank, nc);
+        return outer_item(rows, s_order, item, ablocks, blocks, rblocks, pa.C, pb.C, rank, nc);
     };
     float sum[kOuterCols / 32][16];
     if (warp < 4) {
         int c = 0;  // chains so far
         bool ok = true;
-        for (int64_t item = item0; item < items; item += step_items) {
-            const OuterItem o = item_at(item);
+        for (int64_t round = 0; round * step_items < items; ++round) {
+            if (item_of(round) >= items) continue;
+            const OuterItem o = item_at(item_of(round));
 #pragma unroll
             for (int j = 0; j < kOuterCols / 32; ++j)
 #pragma unroll
@@ -1236,8 +1261,9 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
         const int T = static_cast<int>(rows.T);
         int st = 0, turn = 0;
         bool ok = true, waited = false;
-        for (int64_t item = item0; item < items && ok; item += step_items) {
-            const OuterItem o = item_at(item);
+        for (int64_t round = 0; round * step_items < items && ok; ++round) {
+            if (item_of(round) >= items) continue;
+            const OuterItem o = item_at(item_of(round));
             const uint16_t* const px = o.first ? pa.x : pb.x;
             const int64_t ldx = o.first ? pa.ldx : pb.ldx;
             const Terms pv = o.first ? pa.v : pb.v;
@@ -1305,8 +1331,9 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
         const uint64_t dv0 = sw128_mnmajor_desc(ring_s + kOuterV, kOuterPanel);
         int st = 0, turn = 0, c = 0;
         bool ok = true;
-        for (int64_t item = item0; item < items && ok; item += step_items) {
-            const OuterItem o = item_at(item);
+        for (int64_t round = 0; round * step_items < items && ok; ++round) {
+            if (item_of(round) >= items) continue;
+            const OuterItem o = item_at(item_of(round));
             int step = 0;
             for (int i = 0; i < o.stages; ++i) {
                 if (step == 0 && c >= 2) ok = ok && wait(&s_read[c & 1], (c >> 1) - 1);
@@ -1543,12 +1570,20 @@ cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, c
     const int ab = (a.C + kOuterCols - 1) / kOuterCols, bb = (b.C + kOuterCols - 1) / kOuterCols;
     DeviceInfo di;
     if (!device_info(&di)) return cudaErrorUnknown;
-    // persistent blocks where there are two items for each; else clusters that
-    // share an item's tokens, as many blocks as the GPU holds
+    // Persistent blocks, one item after the other, or clusters of nc blocks that
+    // share an item's tokens: whichever takes fewer stages in a row, a cluster's
+    // start, end and join counted as ten (a stage takes about 0.6 us).
     const int64_t items = static_cast<int64_t>(ab + bb) * rblocks * rows.n, resident = 2 * di.sm_count;
+    const int64_t each = ceil_div64(rows.T, static_cast<int64_t>(kOuterTokens) * rows.n);
     int nc = 1;
-    if (items < 2 * resident)
-        while (nc < 8 && items * nc * 2 <= 2 * resident && rows.T >= 2 * static_cast<int64_t>(nc) * rows.n * 64) nc *= 2;
+    int64_t best = ceil_div64(items, resident) * each + 8;
+    for (int n = 2; n <= 8; n *= 2) {
+        const int64_t cost = ceil_div64(items * n, resident) * (ceil_div64(each, n) + 10);
+        if (cost < best) {
+            best = cost;
+            nc = n;
+        }
+    }
     const int64_t grid = nc > 1 ? items * nc : items < resident ? items : resident;
     OuterSide side[2];
     CUtensorMap map[2];
