@@ -172,25 +172,40 @@ def _refuse(what: str, detail: str):
     raise MoeError(1, what, detail)
 
 
+def _refuse_arg(what: str, name: str, t, dtype, shape, dev: int, how: str):
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or t.get_device() == dev:
+        _refuse(what, f"{name}: expected {dtype} {tuple(shape)} with {how}, got {t.dtype} {tuple(t.shape)}"
+                      f" with strides {t.stride()}")
+    _refuse(what, f"{name} is on {t.device}, not on CUDA device {dev}")
+
+
+# The checks below run on every call, next to kernels of a few microseconds:
+# one pass over what has to hold, the explanation only where something does not.
+
 def _arg(what: str, name: str, t, dtype, shape, dev: int):
     """Address of a contiguous tensor after checking its type, shape and
     device (dev: a CUDA device index)."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _refuse(what, f"{name}: expected contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}"
-                      f" with strides {t.stride()}")
-    if t.get_device() != dev:
-        _refuse(what, f"{name} is on {t.device}, not on CUDA device {dev}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _refuse_arg(what, name, t, dtype, shape, dev, "contiguous elements")
 
 
 def _rows(what: str, name: str, t, dtype, T: int, C: int, dev: int):
     """Address and row stride of a [T, C] tensor whose rows are contiguous."""
-    if t.dtype is not dtype or t.shape != (T, C) or (C > 1 and T > 0 and t.stride(1) != 1):
-        _refuse(what, f"{name}: expected {dtype} ({T}, {C}) with contiguous rows, got {t.dtype} {tuple(t.shape)}"
-                      f" with strides {t.stride()}")
-    if t.get_device() != dev:
-        _refuse(what, f"{name} is on {t.device}, not on CUDA device {dev}")
-    return t.data_ptr(), (t.stride(0) if T > 1 else C)
+    if t.dtype is dtype and t.shape == (T, C) and t.get_device() == dev:
+        if t.is_contiguous():
+            return t.data_ptr(), C
+        ld, one = t.stride()
+        if one == 1 or C == 1 or T == 0:
+            return t.data_ptr(), (ld if T > 1 else C)
+    _refuse_arg(what, name, t, dtype, (T, C), dev, "contiguous rows")
+
+
+def _bytes(what: str, t, dev: int):
+    """Address and size of a contiguous workspace."""
+    if not t.is_contiguous() or t.get_device() != dev:
+        _refuse(what, f"ws: expected a contiguous tensor on CUDA device {dev}, got {t.device}, strides {t.stride()}")
+    return t.data_ptr(), t.nbytes
 
 
 def _device(what: str, name: str, t) -> int:
@@ -200,16 +215,23 @@ def _device(what: str, name: str, t) -> int:
     return dev
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(fn, what: str, dev: int, stream, *args):
     """fn(*args, stream) with dev current; stream: dev's current one if None."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        s = _raw_stream(dev)
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if dev == torch.cuda.current_device():
-        _check(fn(*args, s), what)
+        code = fn(*args, s)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, s), what)
+            code = fn(*args, s)
+    if code:
+        _check(code, what)
 
 
 # ------------------------------------------------------------------ sizes
@@ -557,7 +579,7 @@ def moe_balance_loss(logits, expert_offsets, loss, counts, prob_mean, ws, stream
     _call(lib().moe_balance_loss, what, dev, stream, _arg(what, "logits", logits, f32, (T, E), dev), T, E,
           _arg(what, "expert_offsets", expert_offsets, i32, (E + 1,), dev), _arg(what, "loss", loss, f32, (2,), dev),
           _arg(what, "counts", counts, i32, (E + 1,), dev), _arg(what, "prob_mean", prob_mean, f32, (E,), dev),
-          _arg(what, "ws", ws, ws.dtype, ws.shape, dev), ws.numel() * ws.element_size())
+          *_bytes(what, ws, dev))
 
 
 def moe_route_backward(logits, topk_ids, topk_w, y, dout, routed_scaling, counts, d_loss, d_logits, stream=None):
@@ -640,8 +662,7 @@ def moe_lora_backward(x, lora_a, lora_b, scales, adapter_offsets, sorted_tokens,
           _arg(what, "adapter_offsets", adapter_offsets, i32, (n + 1,), dev),
           _arg(what, "sorted_tokens", sorted_tokens, i32, (T,), dev), _arg(what, "v", v, f32, (T, R), dev), p_dout,
           ld_dout, p_base, ld_base, p_dx, ld_dx, _arg(what, "d_a", d_a, f32, (n, R, K), dev),
-          _arg(what, "d_b", d_b, f32, (n, R, N), dev), _arg(what, "ws", ws, ws.dtype, ws.shape, dev),
-          ws.numel() * ws.element_size())
+          _arg(what, "d_b", d_b, f32, (n, R, N), dev), *_bytes(what, ws, dev))
 
 
 # ------------------------------------------------------------------ layer

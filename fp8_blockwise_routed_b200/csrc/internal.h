@@ -4,6 +4,7 @@
 #include <cuda.h>  // CUtensorMap (types only; libcuda is not linked)
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -59,6 +60,22 @@ struct DeviceInfo {
 };
 // Cached per device; returns false if the current device cannot be queried.
 bool device_info(DeviceInfo* out);
+
+// Dynamic shared memory beyond 48 KB is an attribute of a kernel on a device:
+// set once for each (host threads may launch concurrently).
+template <auto kernel>
+cudaError_t allow_smem(size_t bytes)
+{
+    static std::atomic<bool> done[64];  // one set per kernel
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const bool kept = dev >= 0 && dev < 64;
+    if (bytes <= 48 * 1024 || (kept && done[dev].load(std::memory_order_acquire))) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (err == cudaSuccess && kept) done[dev].store(true, std::memory_order_release);
+    return err;
+}
 
 cudaError_t launch_quant_act(const uint16_t* x, int64_t T, int H, uint8_t* codes, float* scales, cudaStream_t s);
 cudaError_t launch_encode(const float* in, int64_t n, uint8_t* out, cudaStream_t s);

@@ -1434,15 +1434,6 @@ struct Launch {
     }
 };
 
-// Dynamic shared memory beyond 48 KB is a per-device attribute of a kernel.
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes)
-{
-    return bytes <= 48 * 1024 ? cudaSuccess
-                              : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(bytes));
-}
-
 // Blocks per cluster (they share the columns): enough to give every SM two
 // blocks, while each block keeps `least` column steps.
 int cluster_size(int64_t units, int steps, int least, int sm_count)
@@ -1482,7 +1473,7 @@ cudaError_t shrink_tile(const LoraRows& rows, const uint16_t* x, int64_t ldx, in
     const int nc = cluster_size(units, (C + 63) / 64, 4, sm_count);
     CUtensorMap map;
     if (!rank_map(&map, rows, w, R, C, RP)) return cudaErrorNotSupported;
-    cudaError_t err = allow_smem(lora_shrink_tile_kernel<RP>, tile_smem(RP));
+    cudaError_t err = allow_smem<lora_shrink_tile_kernel<RP>>(tile_smem(RP));
     if (err != cudaSuccess) return err;
     Launch l(units * nc, kTileThreads, tile_smem(RP), s, nc, false);
     return cudaLaunchKernelEx(&l.cfg, lora_shrink_tile_kernel<RP>, map, rows, x, ldx, C, R, scales, v, t, u, ut);
@@ -1495,7 +1486,7 @@ cudaError_t expand_tile(const LoraRows& rows, const float* v, int R, const uint1
 {
     CUtensorMap map;
     if (!rank_map(&map, rows, w, R, C, RP)) return cudaErrorNotSupported;
-    cudaError_t err = allow_smem(lora_expand_tile_kernel<RP>, wide_smem(RP));
+    cudaError_t err = allow_smem<lora_expand_tile_kernel<RP>>(wide_smem(RP));
     if (err != cudaSuccess) return err;
     Launch l(sm_count, kWideThreads, wide_smem(RP), s, 0, true);
     return cudaLaunchKernelEx(&l.cfg, lora_expand_tile_kernel<RP>, map, rows, v, R, C, scales, base, ld_base, out,
@@ -1509,7 +1500,7 @@ cudaError_t expand(const LoraRows& rows, const float* v, int R, const uint16_t* 
     const int cols = kExpandThreads / 32 * 8 * NW;
     const int cblocks = (C + cols - 1) / cols;
     constexpr int smem = expand_smem<KS, NW, BT, RING>();
-    cudaError_t err = allow_smem(lora_expand_kernel<KS, NW, BT, RING>, smem);
+    cudaError_t err = allow_smem<lora_expand_kernel<KS, NW, BT, RING>>(smem);
     if (err != cudaSuccess) return err;
     Launch l(max_tiles(rows.T, rows.n, BT) * cblocks, kExpandThreads, smem, s, 0, true);
     return cudaLaunchKernelEx(&l.cfg, lora_expand_kernel<KS, NW, BT, RING>, rows, v, R, w, C, cblocks, scales, base, ld_base,
@@ -1594,7 +1585,7 @@ cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, c
         const uint64_t dims[3] = {row, t1, 3}, strides[2] = {row, t1 * row};
         if (!make_tmap_u8(&map[i], o.v_terms, 3, dims, strides, kOuterTokens)) return cudaErrorNotSupported;
     }
-    cudaError_t err = allow_smem(lora_outer_kernel, kOuterSmem);
+    cudaError_t err = allow_smem<lora_outer_kernel>(kOuterSmem);
     if (err != cudaSuccess) return err;
     Launch l(grid, kOuterThreads, kOuterSmem, s, nc, true);
     return cudaLaunchKernelEx(&l.cfg, lora_outer_kernel, map[0], map[1], rows, R, rblocks, side[0], side[1], ab,
