@@ -203,9 +203,9 @@ size_t ffn_mx_workspace_layout(int64_t T, int H, int I, int k, size_t* off_a, si
                                size_t* off_sh);
 cudaError_t launch_grouped_ffn_mx(const FfnMxArgs& a, cudaStream_t s);
 
-// Balance loss: at most this many blocks sum the probabilities (two per SM
-// of a B200), so the partial sums and their order do not depend on T beyond it.
-constexpr int kLossMaxBlocks = 296;
+// Balance loss: at most this many blocks sum the probabilities (one per SM of a
+// B200), so the partial sums and their order do not depend on T beyond it.
+constexpr int kLossMaxBlocks = 148;
 // Workspace: FP64 lse^2 sums, token counts, probability sums [blocks, E].
 size_t balance_ws_layout(int64_t T, int E, size_t* off_n, size_t* off_part);
 cudaError_t launch_balance_loss(const float* logits, int64_t T, int E, const int32_t* offsets, float* loss,

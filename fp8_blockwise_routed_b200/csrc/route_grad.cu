@@ -61,6 +61,13 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
     }
 }
 
+__device__ __forceinline__ float lg2_approx(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v)
 {
@@ -77,14 +84,37 @@ __device__ __forceinline__ float row_max(float v)
     return v;
 }
 
-// Softmax of a row over its selectable entries (fmaxf drops NaN), in place, 0
-// where not selectable; returns whether there is any, and log(sum exp) in lse.
+// a * b + c and a + b on two neighbours at once.
+__device__ __forceinline__ void fma2(float& x, float& y, float a0, float a1, float b, float c0, float c1)
+{
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a0, float a1)
+{
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "add.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a0), "f"(a1));
+}
+
+// Softmax of a row over its selectable entries (fmaxf drops NaN): v becomes
+// the exponentials, 0 where not selectable, and inv what they are to be
+// multiplied by; returns whether there is any, and log(sum exp) in lse.
 // 2^(v L - mL), L = log2 e, mL = m L rounded: the rounding of mL is the same
 // for the whole row, so it cancels in the probabilities, and its effect on
-// the sum is known exactly (delta) and taken out of the logarithm.  A +Inf
-// logit gives NaN (Inf - Inf), as in the router's weights.
+// the sum is known exactly (delta) and taken out of the logarithm.  The sum
+// lies in [1, E], where lg2.approx is within 2^-22 and one Newton step makes
+// rcp.approx good to an ulp.  A +Inf logit gives NaN (Inf - Inf), as in the
+// router's weights.
 template <int VPL, int LPR>
-__device__ __forceinline__ bool softmax_row(float (&v)[VPL], float& lse)
+__device__ __forceinline__ bool softmax_row(float (&v)[VPL], float& inv, float& lse)
 {
     constexpr float kL = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
     float m = -INFINITY;
@@ -96,26 +126,27 @@ __device__ __forceinline__ bool softmax_row(float (&v)[VPL], float& lse)
     m = row_max<LPR>(m);
     const bool any = m != -INFINITY;
     const float mL = m * kL;
-    float sum = 0.0f, delta = 0.0f;
+    float s0 = 0.0f, s1 = 0.0f, delta = 0.0f;
     if (fabsf(mL) < INFINITY) {
         delta = fmaf(m, kL, -mL);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            v[i] = sm100::ex2_approx_ftz(fmaf(v[i], kL, -mL));
-            sum += v[i];
+        for (int i = 0; i < VPL; i += 2) {
+            fma2(v[i], v[i + 1], v[i], v[i + 1], kL, -mL, -mL);
+            v[i] = sm100::ex2_approx_ftz(v[i]);
+            v[i + 1] = sm100::ex2_approx_ftz(v[i + 1]);
+            add2(s0, s1, v[i], v[i + 1]);
         }
     } else {  // a maximum beyond FP32's range divided by L, an infinite one, or none
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             v[i] = any ? sm100::ex2_approx_ftz((v[i] - m) * kL) : 0.0f;
-            sum += v[i];
+            s0 += v[i];
         }
     }
-    sum = row_sum<LPR>(sum);
-    const float inv = any ? __fdiv_rn(1.0f, sum) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] *= inv;
-    lse = any ? m + (logf(sum) - delta * kLn2) : 0.0f;
+    const float sum = row_sum<LPR>(s0 + s1);
+    inv = sm100::rcp_approx_ftz(sum);
+    inv = any ? fmaf(inv, fmaf(-sum, inv, 1.0f), inv) : 0.0f;
+    lse = any ? m + (lg2_approx(sum) - delta) * kLn2 : 0.0f;
     return any;
 }
 
@@ -123,57 +154,60 @@ __device__ __forceinline__ bool softmax_row(float (&v)[VPL], float& lse)
 
 constexpr int kLossWarps = 16;
 
-// Sums over a block's rows: probabilities into s_sum [E], lse^2 and the number
-// of counted rows returned to every thread.  Rows are dealt to warps (and to
-// the 32 / LPR groups of a warp) block by block; the next row is on its way
-// while one is summed.
+// What a warp gathers over its rows.
+template <int VPL>
+struct WarpSums {
+    float acc[VPL];  // probabilities
+    double z = 0.0;  // lse^2 (short FP32 sums, FP64 beyond)
+    float zf = 0.0f;
+    int n = 0;       // counted rows
+
+    __device__ __forceinline__ WarpSums()
+    {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
+    }
+    template <int LPR>
+    __device__ __forceinline__ void add(float (&v)[VPL])
+    {
+        float inv, lse;
+        if (softmax_row<VPL, LPR>(v, inv, lse)) {
+            zf = fmaf(lse, lse, zf);
+            if ((++n & 15) == 0) {
+                z += zf;
+                zf = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; i += 2) fma2(acc[i], acc[i + 1], v[i], v[i + 1], inv, acc[i], acc[i + 1]);
+    }
+};
+
+// A block's sums from its warps', in warp order: probabilities into s_sum [E],
+// lse^2 and the number of counted rows to every thread.
 struct LossSums {
     double z;
     int n;
 };
 template <int VPL, int LPR>
-__device__ __forceinline__ LossSums loss_sums(const float* __restrict__ logits, int64_t T, int E, int block, int blocks,
-                                              float* s_sum)
+__device__ __forceinline__ LossSums join_warps(WarpSums<VPL>& w, int E, float* s_sum)
 {
-    constexpr int kRows = 32 / LPR;
     __shared__ __align__(16) float red[kLossWarps][256];
     __shared__ double red_z[kLossWarps];
     __shared__ int red_n[kLossWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float acc[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
-    double z = 0.0;
-    int n = 0;
-    const int64_t step = static_cast<int64_t>(blocks) * kLossWarps * kRows;
-    int64_t t = (static_cast<int64_t>(block) * kLossWarps + warp) * kRows;  // the warp's first row
-    const int64_t mine = lane / LPR;
-    float next[VPL];
-    load_row<VPL, LPR>(logits + (t + mine) * E, E, lane, t + mine < T, next);
-    for (; t < T; t += step) {
-        float v[VPL];
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) v[i] = next[i];
-        load_row<VPL, LPR>(logits + (t + step + mine) * E, E, lane, t + step + mine < T, next);
-        float lse;
-        if (softmax_row<VPL, LPR>(v, lse)) {
-            z += static_cast<double>(lse) * lse;
-            ++n;
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] += v[i];
-    }
-    // the groups of a warp, then the warps in order, 256 experts at a time
+    double z = w.z + w.zf;
+    // the groups of a warp, then the warps, 256 experts at a time
 #pragma unroll
     for (int off = LPR; off < 32; off <<= 1) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], off);
+        for (int i = 0; i < VPL; ++i) w.acc[i] += __shfl_xor_sync(0xFFFFFFFFu, w.acc[i], off);
         z += __shfl_xor_sync(0xFFFFFFFFu, z, off);
-        n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
+        w.n += __shfl_xor_sync(0xFFFFFFFFu, w.n, off);
     }
     if (lane == 0) {
         red_z[warp] = z;
-        red_n[warp] = n;
+        red_n[warp] = w.n;
     }
     constexpr int kPart = VPL * LPR < 256 ? VPL * LPR : 256;
 #pragma unroll
@@ -185,7 +219,7 @@ __device__ __forceinline__ LossSums loss_sums(const float* __restrict__ logits, 
                 const int e = expert_of<LPR>(lane, i);
                 if (e >= e0 && e < e0 + kPart)
                     *reinterpret_cast<float4*>(&red[warp][e - e0]) =
-                        make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                        make_float4(w.acc[i], w.acc[i + 1], w.acc[i + 2], w.acc[i + 3]);
             }
         }
         __syncthreads();
@@ -193,21 +227,46 @@ __device__ __forceinline__ LossSums loss_sums(const float* __restrict__ logits, 
         if (threadIdx.x < kPart && e < E) {
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kLossWarps; ++w) s += red[w][threadIdx.x];
+            for (int q = 0; q < kLossWarps; ++q) s += red[q][threadIdx.x];
             s_sum[e] = s;
         }
     }
     __syncthreads();
     LossSums out{0.0, 0};
 #pragma unroll
-    for (int w = 0; w < kLossWarps; ++w) {
-        out.z += red_z[w];
-        out.n += red_n[w];
+    for (int q = 0; q < kLossWarps; ++q) {
+        out.z += red_z[q];
+        out.n += red_n[q];
     }
     return out;
 }
 
-__device__ __forceinline__ double block_sum(double v, double* s_red)  // kLossWarps warps
+// Rows dealt to the blocks' warps (and to the 32 / LPR groups of a warp) one at
+// a time, read straight into registers, the next while one is summed: for few
+// rows, and for row lengths that bulk copies cannot take.
+template <int VPL, int LPR>
+__device__ __forceinline__ LossSums loss_sums(const float* __restrict__ logits, int64_t T, int E, int block, int blocks,
+                                              float* s_sum)
+{
+    constexpr int kRows = 32 / LPR;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    WarpSums<VPL> sums;
+    const int64_t step = static_cast<int64_t>(blocks) * kLossWarps * kRows;
+    int64_t t = (static_cast<int64_t>(block) * kLossWarps + warp) * kRows;  // the warp's first row
+    const int64_t mine = lane / LPR;
+    float next[VPL];
+    load_row<VPL, LPR>(logits + (t + mine) * E, E, lane, t + mine < T, next);
+    for (; t < T; t += step) {
+        float v[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] = next[i];
+        load_row<VPL, LPR>(logits + (t + step + mine) * E, E, lane, t + step + mine < T, next);
+        sums.template add<LPR>(v);
+    }
+    return join_warps<VPL, LPR>(sums, E, s_sum);
+}
+
+__device__ __forceinline__ double block_sum(double v, double* s_red)  // kLossWarps warps, every thread gets it
 {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
@@ -223,6 +282,7 @@ __device__ __forceinline__ double block_sum(double v, double* s_red)  // kLossWa
 // Few rows: one cluster of up to eight blocks does the whole loss in one
 // launch.  Each block sums the experts of its share over the cluster, in
 // block order.
+constexpr int kSmallBlocks = 8;
 template <int VPL, int LPR>
 __global__ void __launch_bounds__(kLossWarps * 32)
     balance_small_kernel(const float* __restrict__ logits, int64_t T, int E, const int32_t* __restrict__ offsets,
@@ -230,7 +290,7 @@ __global__ void __launch_bounds__(kLossWarps * 32)
 {
     __shared__ float s_sum[VPL * LPR];
     __shared__ LossSums s_all;
-    __shared__ double s_term[8];
+    __shared__ double s_term[kSmallBlocks];
     __shared__ double s_red[kLossWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -270,6 +330,17 @@ __global__ void __launch_bounds__(kLossWarps * 32)
 
 // Many rows: per-block sums part [gridDim.x][E], part_z, part_n ...
 template <int VPL, int LPR>
+__device__ __forceinline__ void write_part(const LossSums& own, const float* s_sum, int E, float* __restrict__ part,
+                                           double* __restrict__ part_z, int* __restrict__ part_n)
+{
+    for (int e = threadIdx.x; e < E; e += kLossWarps * 32) part[static_cast<int64_t>(blockIdx.x) * E + e] = s_sum[e];
+    if (threadIdx.x == 0) {
+        part_z[blockIdx.x] = own.z;
+        part_n[blockIdx.x] = own.n;
+    }
+}
+
+template <int VPL, int LPR>
 __global__ void __launch_bounds__(kLossWarps * 32)
     balance_partial_kernel(const float* __restrict__ logits, int64_t T, int E, float* __restrict__ part,
                            double* __restrict__ part_z, int* __restrict__ part_n)
@@ -277,11 +348,100 @@ __global__ void __launch_bounds__(kLossWarps * 32)
     __shared__ float s_sum[VPL * LPR];
     allow_next();
     const LossSums own = loss_sums<VPL, LPR>(logits, T, E, blockIdx.x, gridDim.x, s_sum);
-    for (int e = threadIdx.x; e < E; e += kLossWarps * 32) part[static_cast<int64_t>(blockIdx.x) * E + e] = s_sum[e];
-    if (threadIdx.x == 0) {
-        part_z[blockIdx.x] = own.z;
-        part_n[blockIdx.x] = own.n;
+    write_part<VPL, LPR>(own, s_sum, E, part, part_z, part_n);
+}
+
+// The same by bulk copies, for rows of whole 16-byte pieces: every warp has a
+// ring of its own, chunks of `rows` consecutive rows (4 KB at most), of which
+// up to two are on their way while one is summed.  (With the next row in
+// registers instead, a warp has 1 KB on its way at 256 experts and waits for
+// it: 131072 x 256 in 40 us against %STEP%.)
+constexpr int kLossRing = 3;
+constexpr int kLossChunk = 4096;  // bytes
+constexpr uint64_t kLossWaitNs = 2000000000ull;
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+template <int VPL>
+constexpr int rows_at_once()  // rows that a lane works on side by side
+{
+    return VPL <= 8 ? 2 : 1;
+}
+
+template <int VPL, int LPR>
+__global__ void __launch_bounds__(kLossWarps * 32)
+    balance_bulk_kernel(const float* __restrict__ logits, int64_t T, int E, int rows, float* __restrict__ part,
+                        double* __restrict__ part_z, int* __restrict__ part_n)
+{
+    constexpr int kGroups = 32 / LPR, kOnce = rows_at_once<VPL>();
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float s_sum[VPL * LPR];
+    __shared__ __align__(8) uint64_t s_bar[kLossWarps][kLossRing];
+    __shared__ int s_abort;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    allow_next();
+    if (lane == 0) {
+        for (int i = 0; i < kLossRing; ++i) sm100::mbar_init(sm100::smem_u32(&s_bar[warp][i]), 1);
+        sm100::fence_barrier_init();
     }
+    if (threadIdx.x == 0) s_abort = 0;
+    __syncthreads();
+    uint8_t* const mine = ring + warp * kLossRing * kLossChunk;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kLossWarps * rows;
+    const int64_t t0 = (static_cast<int64_t>(warp) * gridDim.x + blockIdx.x) * rows;
+    auto fetch = [&](int64_t t, int slot) {
+        if (lane == 0 && t < T) {
+            const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(rows), T - t)) * E * 4;
+            const uint32_t bar = sm100::smem_u32(&s_bar[warp][slot]);
+            sm100::mbar_arrive_expect_tx(bar, bytes);
+            bulk_load(sm100::smem_u32(mine) + slot * kLossChunk, logits + t * E, bytes, bar);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kLossRing; ++i) fetch(t0 + i * step, i);
+    WarpSums<VPL> sums;
+    int slot = 0, turn = 0;
+    bool ok = true;
+    for (int64_t t = t0; t < T; t += step) {
+        ok = ok && sm100::mbar_wait_bounded(sm100::smem_u32(&s_bar[warp][slot]), turn & 1, &s_abort, kLossWaitNs);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        const int have = static_cast<int>(min(static_cast<int64_t>(rows), T - t));
+        const float* const chunk = reinterpret_cast<const float*>(mine + slot * kLossChunk);
+        for (int r0 = 0; r0 < have; r0 += kGroups * kOnce) {
+            float v[kOnce][VPL];
+#pragma unroll
+            for (int o = 0; o < kOnce; ++o) {
+                const int r = r0 + o * kGroups + lane / LPR;
+#pragma unroll
+                for (int i = 0; i < VPL; i += 4) {
+                    const int e = expert_of<LPR>(lane, i);
+                    const float4 q = (r < have && e < E)
+                                         ? *reinterpret_cast<const float4*>(chunk + r * E + e)
+                                         : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                    v[o][i] = q.x;
+                    v[o][i + 1] = q.y;
+                    v[o][i + 2] = q.z;
+                    v[o][i + 3] = q.w;
+                }
+            }
+#pragma unroll
+            for (int o = 0; o < kOnce; ++o) sums.template add<LPR>(v[o]);
+        }
+        __syncwarp();
+        fetch(t + kLossRing * step, slot);
+        if (++slot == kLossRing) {
+            slot = 0;
+            ++turn;
+        }
+    }
+    if (!ok) sums.z = NAN;  // a wait that ran out
+    const LossSums own = join_warps<VPL, LPR>(sums, E, s_sum);
+    write_part<VPL, LPR>(own, s_sum, E, part, part_z, part_n);
 }
 
 // ... summed by one cluster of eight blocks, which share the experts; the
@@ -380,10 +540,13 @@ template <int VPL, int LPR>
 __device__ __forceinline__ void grad_row(float (&v)[VPL], const float (&g)[VPL], float zc, int E, int k, int slot_id,
                                          float slot_d, float* __restrict__ dst, int lane, bool ok)
 {
-    float lse, inner = 0.0f;
-    softmax_row<VPL, LPR>(v, lse);
+    float inv, lse, inner = 0.0f;
+    softmax_row<VPL, LPR>(v, inv, lse);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) inner += v[i] * g[i];
+    for (int i = 0; i < VPL; ++i) {
+        v[i] *= inv;
+        inner += v[i] * g[i];
+    }
     inner = row_sum<LPR>(inner) - zc * lse;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) v[i] *= g[i] - inner;
@@ -424,13 +587,6 @@ constexpr int kMaxStages = 16;
 constexpr int kDotBufs = 8;      // tokens between dots and tails
 constexpr int kGradRing = 200 * 1024;
 constexpr uint64_t kGradWaitNs = 2000000000ull;
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 
 template <int VPL>
 __global__ void __launch_bounds__(kGradThreads, 1)
@@ -607,12 +763,11 @@ __global__ void __launch_bounds__(kBalanceGradThreads)
     }
 }
 
-// Blocks of the two-launch loss: two per SM, or one while they have no more
-// than two rows per warp.
+// Blocks of the two-launch loss.
 int64_t loss_blocks(int64_t T)
 {
     const int64_t want = ceil_div64(T > 0 ? T : 1, kLossWarps);
-    return want <= kLossMaxBlocks ? (want < kLossMaxBlocks / 2 ? want : kLossMaxBlocks / 2) : kLossMaxBlocks;
+    return want < kLossMaxBlocks ? want : kLossMaxBlocks;
 }
 
 // One cluster while the logits take no longer to read through eight SMs than
@@ -633,14 +788,28 @@ cudaError_t balance(const float* logits, int64_t T, int E, const int32_t* offset
     cfg.numAttrs = 1;
     if (loss_small(T, E)) {
         unsigned nc = 1;  // blocks with four rows per warp or more
-        while (nc < 8 && T > static_cast<int64_t>(nc) * kLossWarps * 4 * (32 / LPR)) nc *= 2;
+        while (nc < kSmallBlocks && T > static_cast<int64_t>(nc) * kLossWarps * 4 * (32 / LPR)) nc *= 2;
         at[0].val.clusterDim.x = nc;
         cfg.gridDim = dim3(nc);
         return cudaLaunchKernelEx(&cfg, balance_small_kernel<VPL, LPR>, logits, T, E, offsets, loss, counts, prob_mean);
     }
     const int nb = static_cast<int>(loss_blocks(T));
-    balance_partial_kernel<VPL, LPR><<<nb, kLossWarps * 32, 0, s>>>(logits, T, E, part, pz, pn);
-    cudaError_t err = cudaGetLastError();
+    cudaError_t err;
+    if (E % 4 == 0) {
+        // rows per chunk: as many as fit, but no more than give every warp one
+        const int once = 32 / LPR * rows_at_once<VPL>();
+        int64_t rows = ceil_div64(T, static_cast<int64_t>(nb) * kLossWarps);
+        rows = ceil_div64(rows, once) * once;
+        const int most = kLossChunk / (4 * E) / once * once;
+        err = allow_smem<balance_bulk_kernel<VPL, LPR>>(kLossWarps * kLossRing * kLossChunk);
+        if (err != cudaSuccess) return err;
+        balance_bulk_kernel<VPL, LPR><<<nb, kLossWarps * 32, kLossWarps * kLossRing * kLossChunk, s>>>(
+            logits, T, E, rows < most ? static_cast<int>(rows) : most, part, pz, pn);
+        err = cudaGetLastError();
+    } else {
+        balance_partial_kernel<VPL, LPR><<<nb, kLossWarps * 32, 0, s>>>(logits, T, E, part, pz, pn);
+        err = cudaGetLastError();
+    }
     if (err != cudaSuccess) return err;
     at[0].val.clusterDim.x = kFinalBlocks;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
