@@ -483,9 +483,21 @@ int moe_lora(const uint16_t* x, int64_t ld_x, int64_t T, int K, const uint16_t* 
     if (int r = check_device()) return r;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LoraRows rows{T, n_adapters, adapter_offsets, sorted_tokens};
-    cudaError_t err = launch_lora_shrink(rows, x, ld_x, K, lora_a, rank, nullptr, v, nullptr, nullptr, nullptr, s);
-    if (err == cudaSuccess)
-        err = launch_lora_expand(rows, v, rank, lora_b, N, scales, base, ld_base, out, ld_out, out_bf16, s);
+    LoraProduct p{};
+    p.x = x;
+    p.ldx = ld_x;
+    p.C1 = K;
+    p.w1 = lora_a;
+    p.v = v;
+    p.w2 = lora_b;
+    p.C2 = N;
+    p.f2 = scales;
+    p.base = base;
+    p.ld_base = ld_base;
+    p.out = out;
+    p.ld_out = ld_out;
+    p.out_bf16 = out_bf16;
+    cudaError_t err = launch_lora(rows, rank, p, s);
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_lora");
 }
 
@@ -519,13 +531,27 @@ int moe_lora_backward(const uint16_t* x, int64_t ld_x, int64_t T, int K, const u
     const LoraRows rows{T, n_adapters, adapter_offsets, sorted_tokens};
     size_t off_dvt, off_vt;
     lora_ws_layout(T, rank, &off_dvt, &off_vt);
-    float* dv = static_cast<float*>(ws);
     uint16_t* dv_terms = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + off_dvt);
     uint16_t* v_terms = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + off_vt);
-    cudaError_t err = cudaSuccess;
-    if (T > 0) err = launch_lora_shrink(rows, dout, ld_dout, N, lora_b, rank, scales, dv, dv_terms, v, v_terms, s);
-    if (err == cudaSuccess && T > 0 && dx)
-        err = launch_lora_expand(rows, dv, rank, lora_a, K, nullptr, dx_base, ld_dx_base, dx, ld_dx, nullptr, s);
+    LoraProduct p{};
+    p.x = dout;
+    p.ldx = ld_dout;
+    p.C1 = N;
+    p.w1 = lora_b;
+    p.f1 = scales;
+    p.v = static_cast<float*>(ws);
+    p.v_terms = dv_terms;
+    p.u = v;
+    p.u_terms = v_terms;
+    if (dx) {
+        p.w2 = lora_a;
+        p.C2 = K;
+        p.base = dx_base;
+        p.ld_base = ld_dx_base;
+        p.out = dx;
+        p.ld_out = ld_dx;
+    }
+    cudaError_t err = T > 0 ? launch_lora(rows, rank, p, s) : cudaSuccess;
     if (err == cudaSuccess)
         err = launch_lora_outer(rows, rank, LoraOuter{dv_terms, x, ld_x, K, nullptr, d_a},
                                 LoraOuter{v_terms, dout, ld_dout, N, scales, d_b}, s);

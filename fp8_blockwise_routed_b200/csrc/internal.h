@@ -236,17 +236,32 @@ struct LoraRows {
     const int32_t* offsets;  // [n + 1]
     const int32_t* tokens;   // [T] sorted tokens
 };
-// v[p, r] = f_a * sum_c x[tok(p), c] w[a, r, c]   (f_a = scales[a] or 1).
+// Both products of a pass, f[a] = 1 where null:
+//   v[p, r] = f1[a] * sum_c x[tok(p), c] w1[a, r, c]
+//   out[t, c] = base[t, c] + f2[a] * sum_r v[p, r] w2[a, r, c]   (w2 null: v only)
 // v_terms, u_terms (nullable, lora_terms_bytes each): the three BF16 terms of
 // v and of the given FP32 rows u [T, R], as launch_lora_outer reads them.
+struct LoraProduct {
+    const uint16_t* x;
+    int64_t ldx;
+    int C1;
+    const uint16_t* w1;
+    const float* f1;
+    float* v;
+    uint16_t* v_terms;
+    const float* u;
+    uint16_t* u_terms;
+    const uint16_t* w2;
+    int C2;
+    const float* f2;
+    const float* base;
+    int64_t ld_base;
+    float* out;
+    int64_t ld_out;
+    uint16_t* out_bf16;
+};
 size_t lora_terms_bytes(int64_t T, int R);
-cudaError_t launch_lora_shrink(const LoraRows& rows, const uint16_t* x, int64_t ldx, int C, const uint16_t* w, int R,
-                               const float* scales, float* v, uint16_t* v_terms, const float* u, uint16_t* u_terms,
-                               cudaStream_t s);
-// out[t, c] = base[t, c] + f_a * sum_r v[p, r] w[a, r, c]
-cudaError_t launch_lora_expand(const LoraRows& rows, const float* v, int R, const uint16_t* w, int C,
-                               const float* scales, const float* base, int64_t ld_base, float* out, int64_t ld_out,
-                               uint16_t* out_bf16, cudaStream_t s);
+cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, cudaStream_t s);
 // d[a, r, c] = f_a * sum_p v[p, r] x[tok(p), c], two such products at once
 struct LoraOuter {
     const uint16_t* v_terms;

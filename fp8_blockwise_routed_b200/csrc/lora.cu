@@ -24,6 +24,7 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include "../../include/fp8moe.h"
 #include "internal.h"
 #include "sm100.cuh"
 
@@ -62,6 +63,10 @@ __device__ __forceinline__ void split3_pair(float a, float b, uint32_t& h, uint3
     rb -= __uint_as_float(m & 0xFFFF0000u);
     l = pack_bf16(ra, rb);
 }
+
+// The two halves of a cluster barrier.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
@@ -239,124 +244,235 @@ __device__ __forceinline__ void split_rows(const float* __restrict__ src, int R,
 // Tiles of bt tokens that T tokens over n adapters can need at most.
 int64_t max_tiles(int64_t T, int n, int bt) { return ceil_div64(T, bt) + (T < n ? T : n); }
 
-// ------------------------------------------------------------------ shrink
+// ------------------------------------------------- few tokens: one launch
 //
-// v[p, r] = f_a sum_c x[tok, c] w[a, r, c], 8 tokens and 16 MR ranks per
-// cluster.  Ranks are the rows of the MMA and tokens its columns; both
-// operands go from global memory to registers in 16-byte pieces, which the
-// free choice of the order of the sum allows: lane q of a quad takes columns
-// 8q .. 8q+7 of a 32-column step as its K indices of two MMAs.  The columns
-// are dealt to the warps of all blocks of the cluster; their sums are joined
-// in shared memory and across the cluster in a fixed order.
-constexpr int kShrinkThreads = 256;
-constexpr int kShrinkTokens = 8;
+// Both products for 8 tokens of one adapter, per cluster.  First v: ranks are
+// the rows of the MMA and tokens its columns; both operands go from global
+// memory to registers in 16-byte pieces, which the free choice of the order of
+// the sum allows: lane q of a quad takes columns 8q .. 8q+7 of a 32-column step
+// as its K indices of two MMAs.  The columns are dealt to the warps of all
+// blocks of the cluster, whose sums are joined in a fixed order in every
+// block, through the cluster's shared memory.  Then the output columns, a
+// slice per block and 64 per warp: columns are the rows of the MMA, two rank
+// rows interleaved per register, and the three terms of v its columns.  The
+// second product's weights are prefetched into L2 while the first runs, so
+// that memory has one stream of weights to bring in, which bounds a decode
+// batch; the wait in the middle is a cluster barrier and not a launch.
+constexpr int kSmallThreads = 256;
+constexpr int kSmallTokens = 8;
+constexpr int kSmallVPitch = 132;  // floats per token of v, off the bank period
+
+// The first product's side and the second's (w2 null: only v is wanted).
+struct SmallArgs {
+    const uint16_t* x;
+    int64_t ldx;
+    int C1;
+    const uint16_t* w1;
+    const float* f1;  // null: 1
+    float* v;
+    Terms terms;
+    const float* u;
+    Terms u_terms;
+    const uint16_t* w2;
+    int C2;
+    const float* f2;
+    const float* base;
+    int64_t ld_base;
+    float* out;
+    int64_t ld_out;
+    uint16_t* out_bf16;
+};
 
 template <int MR>
-__global__ void __launch_bounds__(kShrinkThreads)
-    lora_shrink_kernel(LoraRows rows, const uint16_t* __restrict__ x, int64_t ldx, int C,
-                       const uint16_t* __restrict__ w, int R, int rblocks, const float* __restrict__ scales,
-                       float* __restrict__ v, Terms terms, const float* __restrict__ u, Terms u_terms)
+__global__ void __launch_bounds__(kSmallThreads, 2) lora_small_kernel(LoraRows rows, int R, SmallArgs p)
 {
-    __shared__ float red[kShrinkThreads / 32][MR * 16 * kShrinkTokens];
-    __shared__ float part[MR * 16 * kShrinkTokens];
+    constexpr int kWarps = kSmallThreads / 32;
+    __shared__ float red[kWarps][MR * 16 * kSmallTokens];
+    __shared__ float part[MOE_MAX_LORA_RANK * kSmallTokens];
+    __shared__ __align__(16) float s_v[kSmallTokens * kSmallVPitch];
+    __shared__ int s_tok[kSmallTokens];
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = static_cast<int>(cluster.num_blocks());
     const int rank = static_cast<int>(cluster.block_rank());
-    const int64_t unit = blockIdx.x / nc;
-    allow_next();
-    const Tile tile = find_tile<kShrinkThreads>(rows, kShrinkTokens, unit / rblocks);
+    const Tile tile = find_tile<kSmallThreads>(rows, kSmallTokens, blockIdx.x / nc);
     if (tile.a < 0) return;  // the whole cluster
-    const int r0 = static_cast<int>(unit % rblocks) * MR * 16;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q = lane & 3;
-    const uint16_t* xr = nullptr;
-    if (g < tile.count) {
-        const int tok = __ldg(rows.tokens + tile.p0 + g);
-        if (tok >= 0 && tok < rows.T) xr = x + tok * ldx;
-    }
-    const uint16_t* wa = w + (static_cast<int64_t>(tile.a) * R + r0) * C;
-    float acc[MR][4], sum[MR][4];
+    int tok = (g < tile.count) ? __ldg(rows.tokens + tile.p0 + g) : -1;
+    if (tok < 0 || tok >= rows.T) tok = -1;
+    if (warp == 0 && q == 0) s_tok[g] = tok;
+    // this block's columns of the second product, and its weights on their way
+    const int slice = ((p.C2 / 8 + nc - 1) / nc) * 8;
+    const int c_lo = min(rank * slice, p.C2), c_hi = min(c_lo + slice, p.C2);
+    const uint16_t* const w2 = p.w2 ? p.w2 + static_cast<int64_t>(tile.a) * R * p.C2 : nullptr;
+    if (w2 && c_hi > c_lo)
+        for (int r = tid; r < R; r += kSmallThreads)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(w2 + static_cast<int64_t>(r) * p.C2 + c_lo),
+                         "r"((c_hi - c_lo) * 2)
+                         : "memory");
+    const int chunks = (p.C1 + 31) / 32, step = nc * kWarps;
+    for (int r0 = 0; r0 < R; r0 += MR * 16) {
+        const uint16_t* const wa = p.w1 + (static_cast<int64_t>(tile.a) * R + r0) * p.C1;
+        float acc[MR][4], sum[MR][4];
 #pragma unroll
-    for (int m = 0; m < MR; ++m)
+        for (int m = 0; m < MR; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = sum[m][i] = 0.0f;
-    const int chunks = (C + 31) / 32;
-    int since = 0;
-    const int step = nc * (kShrinkThreads / 32);
-    for (int c = rank * (kShrinkThreads / 32) + warp; c < chunks; c += 2 * step) {
-        uint4 b[2], lo[2][MR], hi[2][MR];
+            for (int i = 0; i < 4; ++i) acc[m][i] = sum[m][i] = 0.0f;
+        int since = 0;
+        for (int c = rank * kWarps + warp; c < chunks; c += 2 * step) {
+            uint4 b[2], lo[2][MR], hi[2][MR];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {  // two column steps' loads in flight
-            const int k = (c + u * step) * 32 + q * 8;
-            const bool in = k < C;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            b[u] = (in && xr) ? ldg16(xr + k) : zero;
+            for (int u = 0; u < 2; ++u) {  // two column steps' loads in flight
+                const int k = (c + u * step) * 32 + q * 8;
+                const bool in = k < p.C1;
+                const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int m = 0; m < MR; ++m) {
-                const int r = m * 16 + g;
-                lo[u][m] = (in && r0 + r < R) ? ldg16(wa + static_cast<int64_t>(r) * C + k) : zero;
-                hi[u][m] = (in && r0 + r + 8 < R) ? ldg16(wa + static_cast<int64_t>(r + 8) * C + k) : zero;
+                for (int m = 0; m < MR; ++m) {
+                    const int r = m * 16 + g;
+                    lo[u][m] = (in && r0 + r < R) ? ldg16(wa + static_cast<int64_t>(r) * p.C1 + k) : zero;
+                    hi[u][m] = (in && r0 + r + 8 < R) ? ldg16(wa + static_cast<int64_t>(r + 8) * p.C1 + k) : zero;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // (their address comes later than the weights')
+                const int k = (c + u * step) * 32 + q * 8;
+                b[u] = (k < p.C1 && tok >= 0) ? ldg16(p.x + tok * p.ldx + k) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int m = 0; m < MR; ++m) {
+                    mma_bf16(acc[m], lo[u][m].x, hi[u][m].x, lo[u][m].y, hi[u][m].y, b[u].x, b[u].y);
+                    mma_bf16(acc[m], lo[u][m].z, hi[u][m].z, lo[u][m].w, hi[u][m].w, b[u].z, b[u].w);
+                }
+            if (++since == 4) {  // short chains on the tensor core, joined in FP32
+                since = 0;
+#pragma unroll
+                for (int m = 0; m < MR; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        sum[m][i] += acc[m][i];
+                        acc[m][i] = 0.0f;
+                    }
             }
         }
+        // element (rank m*16 + g [+8], token 2q [+1]) of the tile
+        if (r0 > 0) __syncthreads();
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int m = 0; m < MR; ++m)
 #pragma unroll
-            for (int m = 0; m < MR; ++m) {
-                mma_bf16(acc[m], lo[u][m].x, hi[u][m].x, lo[u][m].y, hi[u][m].y, b[u].x, b[u].y);
-                mma_bf16(acc[m], lo[u][m].z, hi[u][m].z, lo[u][m].w, hi[u][m].w, b[u].z, b[u].w);
+            for (int i = 0; i < 4; ++i)
+                red[warp][(m * 16 + g + (i >> 1) * 8) * kSmallTokens + 2 * q + (i & 1)] = sum[m][i] + acc[m][i];
+        __syncthreads();
+        for (int e = tid; e < MR * 16 * kSmallTokens; e += kSmallThreads) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += red[w][e];
+            part[r0 * kSmallTokens + e] = s;
+        }
+    }
+    cluster.sync();
+    const float f1 = p.f1 ? __ldg(p.f1 + tile.a) : 1.0f;
+    const int ranks = (R + MR * 16 - 1) / (MR * 16) * MR * 16;  // with the zeros past R
+    for (int e = tid; e < ranks * kSmallTokens; e += kSmallThreads) {
+        float s = 0.0f;
+#pragma unroll 8
+        for (int b = 0; b < nc; ++b) s += cluster.map_shared_rank(part, b)[e];
+        s_v[e % kSmallTokens * kSmallVPitch + e / kSmallTokens] = e / kSmallTokens < R ? f1 * s : 0.0f;
+    }
+    __syncwarp();
+    cluster_arrive();  // the peers' sums are read
+    __syncthreads();
+    // v itself, and its terms, by the blocks in turn
+    for (int e = rank * kSmallThreads + tid; e < tile.count * (ranks / 4); e += nc * kSmallThreads) {
+        const int tk = e / (ranks / 4), r = e % (ranks / 4) * 4;
+        const int64_t at = tile.p0 + tk;
+        const float* s = s_v + tk * kSmallVPitch + r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (r + i < R) p.v[at * R + r + i] = s[i];
+        if (p.terms.at && r < p.terms.R8) p.terms.put4(at, r, s[0], s[1], s[2], s[3]);
+    }
+    if (p.u_terms.at && rank == 0) split_rows(p.u, R, p.u_terms, tile.p0, tile.p0 + tile.count, tid, kSmallThreads);
+    if (w2) {
+        const float f2 = p.f2 ? __ldg(p.f2 + tile.a) : 1.0f;
+        const int tk[2] = {s_tok[2 * q], s_tok[2 * q + 1]};
+        const int steps = ranks / 16;
+        for (int c0 = c_lo + warp * 64; c0 < c_hi; c0 += kWarps * 64) {
+            // tile j: row g is column c0 + 4 g + j, row g + 8 column c0 + 32 + 4 g + j
+            const int ca = c0 + 4 * g, cb = ca + 32;
+            float4 old[2][2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const int c = z ? cb : ca;
+                    old[t][z] = (p.base && tk[t] >= 0 && c < c_hi)
+                                    ? *reinterpret_cast<const float4*>(p.base + tk[t] * p.ld_base + c)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            float acc[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+            for (int s0 = 0; s0 < steps; s0 += MR) {  // MR steps' loads in flight
+                uint2 ra[MR][4], rb[MR][4];
+#pragma unroll
+                for (int s = 0; s < MR; ++s)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 16 * (s0 + s) + 4 * q + i;
+                        const uint16_t* w = w2 + static_cast<int64_t>(r) * p.C2;
+                        ra[s][i] = (r < R && ca < c_hi) ? __ldg(reinterpret_cast<const uint2*>(w + ca)) : make_uint2(0, 0);
+                        rb[s][i] = (r < R && cb < c_hi) ? __ldg(reinterpret_cast<const uint2*>(w + cb)) : make_uint2(0, 0);
+                    }
+#pragma unroll
+                for (int s = 0; s < MR; ++s) {
+                    const float4 vv =
+                        *reinterpret_cast<const float4*>(s_v + g * kSmallVPitch + 16 * (s0 + s) + 4 * q);
+                    uint32_t h[2], m[2], l[2];
+                    split3_pair(vv.x, vv.y, h[0], m[0], l[0]);
+                    split3_pair(vv.z, vv.w, h[1], m[1], l[1]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+                        const bool up = j >= 2;
+                        const uint32_t a0 = __byte_perm(up ? ra[s][0].y : ra[s][0].x, up ? ra[s][1].y : ra[s][1].x, sel);
+                        const uint32_t a1 = __byte_perm(up ? rb[s][0].y : rb[s][0].x, up ? rb[s][1].y : rb[s][1].x, sel);
+                        const uint32_t a2 = __byte_perm(up ? ra[s][2].y : ra[s][2].x, up ? ra[s][3].y : ra[s][3].x, sel);
+                        const uint32_t a3 = __byte_perm(up ? rb[s][2].y : rb[s][2].x, up ? rb[s][3].y : rb[s][3].x, sel);
+                        mma_bf16(acc[j], a0, a1, a2, a3, l[0], l[1]);  // the small terms first
+                        mma_bf16(acc[j], a0, a1, a2, a3, m[0], m[1]);
+                        mma_bf16(acc[j], a0, a1, a2, a3, h[0], h[1]);
+                    }
+                }
             }
-        if (++since == 4) {  // short chains on the tensor core, joined in FP32
-            since = 0;
+            // acc[j][2 z + t]: column (z ? cb : ca) + j of token 2 q + t
 #pragma unroll
-            for (int m = 0; m < MR; ++m)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sum[m][i] += acc[m][i];
-                    acc[m][i] = 0.0f;
+                for (int z = 0; z < 2; ++z) {
+                    const int c = z ? cb : ca;
+                    if (tk[t] < 0 || c >= c_hi) continue;
+                    const float4 o = old[t][z];
+                    const float4 r = make_float4(fmaf(f2, acc[0][2 * z + t], o.x), fmaf(f2, acc[1][2 * z + t], o.y),
+                                                 fmaf(f2, acc[2][2 * z + t], o.z), fmaf(f2, acc[3][2 * z + t], o.w));
+                    *reinterpret_cast<float4*>(p.out + tk[t] * p.ld_out + c) = r;
+                    if (p.out_bf16)
+                        *reinterpret_cast<uint2*>(p.out_bf16 + static_cast<int64_t>(tk[t]) * p.C2 + c) =
+                            make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
                 }
         }
     }
-    // element (rank m*16 + g [+8], token 2q [+1]) of the tile
-#pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            red[warp][(m * 16 + g + (i >> 1) * 8) * kShrinkTokens + 2 * q + (i & 1)] = sum[m][i] + acc[m][i];
-    __syncthreads();
-    constexpr int kElems = MR * 16 * kShrinkTokens;
-    for (int e = threadIdx.x; e < kElems; e += kShrinkThreads) {
-        float s = 0.0f;
-#pragma unroll
-        for (int wi = 0; wi < kShrinkThreads / 32; ++wi) s += red[wi][e];
-        part[e] = s;
-    }
-    cluster.sync();
-    const float f = scales ? __ldg(scales + tile.a) : 1.0f;
-    // four ranks of a token at a time
-    for (int e = rank * kShrinkThreads + threadIdx.x; e < kElems / 4; e += nc * kShrinkThreads) {
-        const int tk = e % kShrinkTokens, r4 = e / kShrinkTokens * 4, r = r0 + r4;
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int b = 0; b < nc; ++b) {
-            const float* q = cluster.map_shared_rank(part, b) + r4 * kShrinkTokens + tk;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] += q[i * kShrinkTokens];
-        }
-        if (tk >= tile.count) continue;
-        const int64_t p = tile.p0 + tk;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s[i] = r + i < R ? f * s[i] : 0.0f;
-            if (r + i < R) v[p * R + r + i] = s[i];
-        }
-        if (terms.at && r < terms.R8) terms.put4(p, r, s[0], s[1], s[2], s[3]);
-    }
-    if (u_terms.at && r0 == 0 && rank == 0)
-        split_rows(u, R, u_terms, tile.p0, tile.p0 + tile.count, threadIdx.x, kShrinkThreads);
-    cluster.sync();  // the peers have read this block's part
+    __syncwarp();
+    cluster_wait();  // no block ends while a peer reads its sums
 }
 
-// The same product for adapters with many tokens: 128 tokens times all ranks
-// per cluster on tcgen05, the columns dealt to the cluster's blocks 64 at a
+// ------------------------------------------------------------------ shrink
+//
+// v[p, r] = f_a sum_c x[tok, c] w[a, r, c] for adapters with many tokens: 128
+// tokens times all ranks per cluster on tcgen05, the columns dealt to the cluster's blocks 64 at a
 // time.  A stage holds the 128 token rows and the RP rank rows of 64 columns
 // (128-byte rows, 128-byte swizzle); four producer warps bring in the token
 // rows by cp.async, which gathers them and zero-fills what is missing, one TMA
@@ -617,7 +733,8 @@ __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
 
 // ------------------------------------------------------------------ expand
 //
-// out[t, c] = base[t, c] + f_a sum_r v[p, r] w[a, r, c].  A warp keeps the
+// out[t, c] = base[t, c] + f_a sum_r v[p, r] w[a, r, c], behind the tiled shrink.
+// A warp keeps the
 // adapter's ranks of 8 NW columns in registers (the B operand, two rank rows
 // interleaved per register) and walks over the tile's tokens, 16 at a time.
 // Tokens are the rows of the MMA; column g of its j-th tile is column
@@ -1453,15 +1570,12 @@ bool rank_map(CUtensorMap* map, const LoraRows& rows, const uint16_t* w, int R, 
 }
 
 template <int MR>
-cudaError_t shrink(const LoraRows& rows, const uint16_t* x, int64_t ldx, int C, const uint16_t* w, int R,
-                   const float* scales, float* v, const Terms& t, const float* u, const Terms& ut, int sm_count,
-                   cudaStream_t s)
+cudaError_t small(const LoraRows& rows, int R, const SmallArgs& p, int sm_count, cudaStream_t s)
 {
-    const int rblocks = (R + 16 * MR - 1) / (16 * MR);
-    const int64_t units = max_tiles(rows.T, rows.n, kShrinkTokens) * rblocks;
-    const int nc = cluster_size(units, (C + 31) / 32, 2 * (kShrinkThreads / 32), sm_count);
-    Launch l(units * nc, kShrinkThreads, 0, s, nc, false);
-    return cudaLaunchKernelEx(&l.cfg, lora_shrink_kernel<MR>, rows, x, ldx, C, w, R, rblocks, scales, v, t, u, ut);
+    const int64_t units = max_tiles(rows.T, rows.n, kSmallTokens);
+    const int nc = cluster_size(units, (p.C1 + 31) / 32, 2 * (kSmallThreads / 32), sm_count);
+    Launch l(units * nc, kSmallThreads, 0, s, nc, false);
+    return cudaLaunchKernelEx(&l.cfg, lora_small_kernel<MR>, rows, R, p);
 }
 
 template <int RP>
@@ -1515,44 +1629,47 @@ Terms terms_at(uint16_t* at, int64_t T, int R) { return Terms{at, T * round8(R),
 
 size_t lora_terms_bytes(int64_t T, int R) { return static_cast<size_t>(T) * round8(R) * 3 * 2; }
 
-cudaError_t launch_lora_shrink(const LoraRows& rows, const uint16_t* x, int64_t ldx, int C, const uint16_t* w, int R,
-                               const float* scales, float* v, uint16_t* v_terms, const float* u, uint16_t* u_terms,
-                               cudaStream_t s)
+cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, cudaStream_t s)
 {
     DeviceInfo di;
     if (!device_info(&di)) return cudaErrorUnknown;
-    const Terms t = terms_at(v_terms, rows.T, R), ut = terms_at(u_terms, rows.T, R);
+    const Terms t = terms_at(p.v_terms, rows.T, R), ut = terms_at(p.u_terms, rows.T, R);
     const int sms = di.sm_count;
-    if (rows.T >= 256 && rows.T >= 16 * static_cast<int64_t>(rows.n)) {
-        if (R <= 16) return shrink_tile<16>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
-        if (R <= 32) return shrink_tile<32>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
-        if (R <= 64) return shrink_tile<64>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
-        return shrink_tile<128>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
+    // Few tokens, or few for each adapter: one launch over tiles of 8 tokens.
+    if (rows.T < 256 || rows.T < 16 * static_cast<int64_t>(rows.n)) {
+        const SmallArgs a{p.x,    p.ldx, p.C1,   p.w1,      p.f1,  p.v,      t,         p.u, ut, p.w2,
+                          p.C2, p.f2,  p.base, p.ld_base, p.out, p.ld_out, p.out_bf16};
+        if (R <= 16) return small<1>(rows, R, a, sms, s);
+        if (R <= 32) return small<2>(rows, R, a, sms, s);
+        return small<4>(rows, R, a, sms, s);
     }
-    if (R <= 16) return shrink<1>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
-    if (R <= 32) return shrink<2>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
-    return shrink<4>(rows, x, ldx, C, w, R, scales, v, t, u, ut, sms, s);
-}
-
-cudaError_t launch_lora_expand(const LoraRows& rows, const float* v, int R, const uint16_t* w, int C,
-                               const float* scales, const float* base, int64_t ld_base, float* out, int64_t ld_out,
-                               uint16_t* out_bf16, cudaStream_t s)
-{
+    cudaError_t err;
+    if (R <= 16)
+        err = shrink_tile<16>(rows, p.x, p.ldx, p.C1, p.w1, R, p.f1, p.v, t, p.u, ut, sms, s);
+    else if (R <= 32)
+        err = shrink_tile<32>(rows, p.x, p.ldx, p.C1, p.w1, R, p.f1, p.v, t, p.u, ut, sms, s);
+    else if (R <= 64)
+        err = shrink_tile<64>(rows, p.x, p.ldx, p.C1, p.w1, R, p.f1, p.v, t, p.u, ut, sms, s);
+    else
+        err = shrink_tile<128>(rows, p.x, p.ldx, p.C1, p.w1, R, p.f1, p.v, t, p.u, ut, sms, s);
+    if (err != cudaSuccess || !p.w2) return err;
     // Ranks above 32 with many tokens per adapter and enough rows to fill the
-    // GPU: the tcgen05 kernel (16384 x 6144, rank 64: 172 us against 220;
-    // 4096 x 5120: 55 against 64; 2048 x 2048: 28.5 against 25).  Up to rank
+    // GPU: the tcgen05 kernel (16384 x 6144, rank 64: 164 us against 220;
+    // 4096 x 5120: 48 against 64; 2048 x 2048: 28 against 25).  Up to rank
     // 32 the register kernel is ahead (rank 16: 136 us against 153).
-    if (R > 32 && rows.T >= 64 * static_cast<int64_t>(rows.n) && rows.T * C >= (int64_t(1) << 24)) {
-        DeviceInfo di;
-        if (!device_info(&di)) return cudaErrorUnknown;
-        return R <= 64 ? expand_tile<64>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, di.sm_count, s)
-                       : expand_tile<128>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, di.sm_count,
-                                          s);
+    if (R > 32 && rows.T >= 64 * static_cast<int64_t>(rows.n) && rows.T * p.C2 >= (int64_t(1) << 24)) {
+        if (R <= 64)
+            return expand_tile<64>(rows, p.v, R, p.w2, p.C2, p.f2, p.base, p.ld_base, p.out, p.ld_out, p.out_bf16, sms,
+                                   s);
+        return expand_tile<128>(rows, p.v, R, p.w2, p.C2, p.f2, p.base, p.ld_base, p.out, p.ld_out, p.out_bf16, sms, s);
     }
-    if (R <= 16) return expand<1, 8, 64, 3>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
-    if (R <= 32) return expand<2, 8, 64, 3>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
-    if (R <= 64) return expand<4, 8, 64, 2>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
-    return expand<8, 4, 32, 3>(rows, v, R, w, C, scales, base, ld_base, out, ld_out, out_bf16, s);
+    if (R <= 16)
+        return expand<1, 8, 64, 3>(rows, p.v, R, p.w2, p.C2, p.f2, p.base, p.ld_base, p.out, p.ld_out, p.out_bf16, s);
+    if (R <= 32)
+        return expand<2, 8, 64, 3>(rows, p.v, R, p.w2, p.C2, p.f2, p.base, p.ld_base, p.out, p.ld_out, p.out_bf16, s);
+    if (R <= 64)
+        return expand<4, 8, 64, 2>(rows, p.v, R, p.w2, p.C2, p.f2, p.base, p.ld_base, p.out, p.ld_out, p.out_bf16, s);
+    return expand<8, 4, 32, 3>(rows, p.v, R, p.w2, p.C2, p.f2, p.base, p.ld_base, p.out, p.ld_out, p.out_bf16, s);
 }
 
 cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, const LoraOuter& b, cudaStream_t s)
