@@ -64,6 +64,11 @@ __device__ __forceinline__ void split3_pair(float a, float b, uint32_t& h, uint3
     l = pack_bf16(ra, rb);
 }
 
+__device__ __forceinline__ float4 add4(const float4& a, const float4& b)
+{
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
 // The two halves of a cluster barrier.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -254,10 +259,10 @@ int64_t max_tiles(int64_t T, int n, int bt) { return ceil_div64(T, bt) + (T < n 
 // blocks of the cluster, whose sums are joined in a fixed order in every
 // block, through the cluster's shared memory.  Then the output columns, a
 // slice per block and 64 per warp: columns are the rows of the MMA, two rank
-// rows interleaved per register, and the three terms of v its columns.  The
-// second product's weights are prefetched into L2 while the first runs, so
-// that memory has one stream of weights to bring in, which bounds a decode
-// batch; the wait in the middle is a cluster barrier and not a launch.
+// rows interleaved per register, and the three terms of v its columns.  A
+// decode batch is bound by bringing the adapters in (64 tokens on 34 adapters
+// of rank 64, 5120 to 5120: %DECODE%); a single token by the steps in a row, where
+// the wait in the middle is a cluster barrier and not a launch.
 constexpr int kSmallThreads = 256;
 constexpr int kSmallTokens = 8;
 constexpr int kSmallVPitch = 132;  // floats per token of v, off the bank period
@@ -287,8 +292,8 @@ template <int MR>
 __global__ void __launch_bounds__(kSmallThreads, 2) lora_small_kernel(LoraRows rows, int R, SmallArgs p)
 {
     constexpr int kWarps = kSmallThreads / 32;
-    __shared__ float red[kWarps][MR * 16 * kSmallTokens];
-    __shared__ float part[MOE_MAX_LORA_RANK * kSmallTokens];
+    __shared__ __align__(16) float red[kWarps][MR * 16 * kSmallTokens];
+    __shared__ __align__(16) float part[MOE_MAX_LORA_RANK * kSmallTokens];
     __shared__ __align__(16) float s_v[kSmallTokens * kSmallVPitch];
     __shared__ int s_tok[kSmallTokens];
     cg::cluster_group cluster = cg::this_cluster();
@@ -301,15 +306,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) lora_small_kernel(LoraRows r
     int tok = (g < tile.count) ? __ldg(rows.tokens + tile.p0 + g) : -1;
     if (tok < 0 || tok >= rows.T) tok = -1;
     if (warp == 0 && q == 0) s_tok[g] = tok;
-    // this block's columns of the second product, and its weights on their way
+    // this block's columns of the second product, dealt evenly to its warps
     const int slice = ((p.C2 / 8 + nc - 1) / nc) * 8;
-    const int c_lo = min(rank * slice, p.C2), c_hi = min(c_lo + slice, p.C2);
+    const int per = ((slice / 8 + kWarps - 1) / kWarps) * 8;
+    const int c_lo = min(rank * slice + warp * per, min((rank + 1) * slice, p.C2));
+    const int c_hi = min(c_lo + per, min((rank + 1) * slice, p.C2));
     const uint16_t* const w2 = p.w2 ? p.w2 + static_cast<int64_t>(tile.a) * R * p.C2 : nullptr;
-    if (w2 && c_hi > c_lo)
-        for (int r = tid; r < R; r += kSmallThreads)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(w2 + static_cast<int64_t>(r) * p.C2 + c_lo),
-                         "r"((c_hi - c_lo) * 2)
-                         : "memory");
     const int chunks = (p.C1 + 31) / 32, step = nc * kWarps;
     for (int r0 = 0; r0 < R; r0 += MR * 16) {
         const uint16_t* const wa = p.w1 + (static_cast<int64_t>(tile.a) * R + r0) * p.C1;
@@ -364,21 +366,43 @@ __global__ void __launch_bounds__(kSmallThreads, 2) lora_small_kernel(LoraRows r
             for (int i = 0; i < 4; ++i)
                 red[warp][(m * 16 + g + (i >> 1) * 8) * kSmallTokens + 2 * q + (i & 1)] = sum[m][i] + acc[m][i];
         __syncthreads();
-        for (int e = tid; e < MR * 16 * kSmallTokens; e += kSmallThreads) {
-            float s = 0.0f;
+        for (int e = tid * 4; e < MR * 16 * kSmallTokens; e += kSmallThreads * 4) {
+            float4 s = *reinterpret_cast<const float4*>(&red[0][e]);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += red[w][e];
-            part[r0 * kSmallTokens + e] = s;
+            for (int w = 1; w < kWarps; ++w) s = add4(s, *reinterpret_cast<const float4*>(&red[w][e]));
+            *reinterpret_cast<float4*>(part + r0 * kSmallTokens + e) = s;
         }
     }
+    // the warp's first weights of the second product are under way during the join
+    uint2 ra[MR][4], rb[MR][4];
+    auto load_w2 = [&](int c0, int s0) {  // 64 columns, MR steps of 16 ranks
+        const int ca = c0 + 4 * g, cb = ca + 32;
+#pragma unroll
+        for (int s = 0; s < MR; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * (s0 + s) + 4 * q + i;
+                const uint16_t* w = w2 + static_cast<int64_t>(r) * p.C2;
+                ra[s][i] = (r < R && ca < c_hi) ? __ldg(reinterpret_cast<const uint2*>(w + ca)) : make_uint2(0, 0);
+                rb[s][i] = (r < R && cb < c_hi) ? __ldg(reinterpret_cast<const uint2*>(w + cb)) : make_uint2(0, 0);
+            }
+    };
+    if (w2) load_w2(c_lo, 0);
     cluster.sync();
     const float f1 = p.f1 ? __ldg(p.f1 + tile.a) : 1.0f;
     const int ranks = (R + MR * 16 - 1) / (MR * 16) * MR * 16;  // with the zeros past R
-    for (int e = tid; e < ranks * kSmallTokens; e += kSmallThreads) {
-        float s = 0.0f;
+    for (int e = tid * 4; e < ranks * kSmallTokens; e += kSmallThreads * 4) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int b = 0; b < nc; ++b) s += cluster.map_shared_rank(part, b)[e];
-        s_v[e % kSmallTokens * kSmallVPitch + e / kSmallTokens] = e / kSmallTokens < R ? f1 * s : 0.0f;
+        for (int b = 0; b < nc; ++b)
+            s = add4(s, *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, b) + e));
+        const int r = e / kSmallTokens;
+        const bool in = r < R;
+        float* const d = s_v + e % kSmallTokens * kSmallVPitch + r;
+        d[0] = in ? f1 * s.x : 0.0f;
+        d[kSmallVPitch] = in ? f1 * s.y : 0.0f;
+        d[2 * kSmallVPitch] = in ? f1 * s.z : 0.0f;
+        d[3 * kSmallVPitch] = in ? f1 * s.w : 0.0f;
     }
     __syncwarp();
     cluster_arrive();  // the peers' sums are read
@@ -398,7 +422,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) lora_small_kernel(LoraRows r
         const float f2 = p.f2 ? __ldg(p.f2 + tile.a) : 1.0f;
         const int tk[2] = {s_tok[2 * q], s_tok[2 * q + 1]};
         const int steps = ranks / 16;
-        for (int c0 = c_lo + warp * 64; c0 < c_hi; c0 += kWarps * 64) {
+        for (int c0 = c_lo; c0 < c_hi; c0 += 64) {
             // tile j: row g is column c0 + 4 g + j, row g + 8 column c0 + 32 + 4 g + j
             const int ca = c0 + 4 * g, cb = ca + 32;
             float4 old[2][2];
@@ -416,17 +440,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) lora_small_kernel(LoraRows r
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-            for (int s0 = 0; s0 < steps; s0 += MR) {  // MR steps' loads in flight
-                uint2 ra[MR][4], rb[MR][4];
-#pragma unroll
-                for (int s = 0; s < MR; ++s)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 16 * (s0 + s) + 4 * q + i;
-                        const uint16_t* w = w2 + static_cast<int64_t>(r) * p.C2;
-                        ra[s][i] = (r < R && ca < c_hi) ? __ldg(reinterpret_cast<const uint2*>(w + ca)) : make_uint2(0, 0);
-                        rb[s][i] = (r < R && cb < c_hi) ? __ldg(reinterpret_cast<const uint2*>(w + cb)) : make_uint2(0, 0);
-                    }
+            for (int s0 = 0; s0 < steps; s0 += MR) {
+                if (c0 != c_lo || s0 != 0) load_w2(c0, s0);
 #pragma unroll
                 for (int s = 0; s < MR; ++s) {
                     const float4 vv =
