@@ -196,9 +196,9 @@ def _rows(what: str, name: str, t, dtype, T: int, C: int, dev: int):
         if t.is_contiguous():
             return t.data_ptr(), C
         ld, one = t.stride()
-        if one == 1 or C == 1 or T == 0:
+        if one == 1 and (T == 1 or ld >= C):
             return t.data_ptr(), (ld if T > 1 else C)
-    _refuse_arg(what, name, t, dtype, (T, C), dev, "contiguous rows")
+    _refuse_arg(what, name, t, dtype, (T, C), dev, "contiguous rows that do not overlap")
 
 
 def _bytes(what: str, t, dev: int):

@@ -489,6 +489,8 @@ MOE_API int moe_combine_rows(const float* y, int64_t y_nrows, const int32_t* row
  *
  * The sums over rows have a fixed order (FP32 inside a block, FP64 across
  * blocks): the same bits on every call.  The call records no device status.
+ * A workspace serves one call in flight (give captured graphs that may replay
+ * side by side one each).
  * Limits: T >= 0, 1 <= E <= 1024.
  * ------------------------------------------------------------------------- */
 MOE_API size_t moe_balance_loss_workspace_bytes(int64_t T, int E);
@@ -540,7 +542,7 @@ MOE_API int moe_route_backward(const float* logits, int64_t T, int E, const int3
  * with exact BF16 products summed in FP32 and v kept in FP32.  Rows of
  * tokens without an adapter are left as they were, as are rows of v at and
  * past adapter_offsets[n_adapters].  A row's bits depend on its adapter's
- * weights and its own inputs only, for one T, n_adapters and rank.
+ * weights and its own inputs only, for one K, N, T, n_adapters and rank.
  *
  *   x               [T, K] BF16 words, row stride ld_x elements, read
  *   lora_a          [n_adapters, rank, K] BF16 words, read
@@ -548,9 +550,11 @@ MOE_API int moe_route_backward(const float* logits, int64_t T, int E, const int3
  *                   transpose of an output projection's [N, rank]
  *   scales          [n_adapters] FP32, read, or NULL (1)
  *   adapter_offsets [n_adapters + 1] int32, read
- *   sorted_tokens   [T] int32, read (entries outside [0, T) are skipped)
+ *   sorted_tokens   [T] int32, read (entries outside [0, T) are skipped; a
+ *                   token appears once)
  *   base            [T, N] FP32, row stride ld_base, read, or NULL (0); may
- *                   be out itself (the product is then added in place)
+ *                   be out itself (the product is then added in place), and
+ *                   overlaps it in no other way
  *   v               [T, rank] FP32, written (kept for moe_lora_backward)
  *   out             [T, N] FP32, row stride ld_out, written: for instance a
  *                   shared-expert slot of y (ld_out = (top_k + 1) * H)
@@ -558,7 +562,9 @@ MOE_API int moe_route_backward(const float* logits, int64_t T, int E, const int3
  *
  * Limits: T >= 0 (at most 2^24); 1 <= n_adapters <= 1024; 1 <= rank <= 128;
  * K, N multiples of 8, 8 .. 16384; ld_x a multiple of 8, ld_base and ld_out
- * of 4.  No workspace, no device status.
+ * of 4.  No workspace, no device status; v and out overlap nothing that is
+ * read (but base).  One to two launches, two or three with the backward call;
+ * a wait inside a kernel that expires leaves NaN in the rows concerned.
  *
  * moe_lora_backward -- its gradients, for dout the gradient of out:
  *   dv[p, r]     = scales[a] * sum_c dout[t, c] lora_b[a, r, c]
@@ -573,7 +579,8 @@ MOE_API int moe_route_backward(const float* logits, int64_t T, int E, const int3
  *               adapter, or NULL: no gradient of x
  *   d_a, d_b    [n_adapters, rank, K] and [n_adapters, rank, N] FP32, written
  *               in full (zeros for an adapter without tokens)
- *   ws          scratch of at least moe_lora_backward_workspace_bytes(T, rank)
+ *   ws          scratch of at least moe_lora_backward_workspace_bytes(T,
+ *               rank), for one call in flight
  * ------------------------------------------------------------------------- */
 MOE_API int moe_lora(const uint16_t* x, int64_t ld_x, int64_t T, int K, const uint16_t* lora_a,
                      const uint16_t* lora_b, const float* scales, int n_adapters, int rank, int N,

@@ -108,7 +108,14 @@ SHAPES = [(1, 8, 8, 1, 1, "one"), (1, 5120, 640, 16, 8, "one"), (5, 24, 40, 3, 2
           (70, 264, 520, 13, 5, "mixed"), (129, 1024, 72, 33, 7, "requests"), (300, 136, 1000, 100, 3, "one"),
           (64, 512, 512, 64, 64, "own"), (17, 5120, 264, 128, 4, "mixed"), (513, 328, 320, 17, 1024, "mixed"),
           (1030, 256, 248, 32, 3, "requests"), (2100, 1536, 1096, 64, 2, "requests"), (40, 64, 64, 8, 4, "none"),
-          (700, 2048, 136, 48, 2, "mixed"), (333, 200, 2056, 24, 300, "own"), (16, 16384, 16384, 8, 3, "mixed")]
+          (700, 2048, 136, 48, 2, "mixed"), (333, 200, 2056, 24, 300, "own"), (16, 16384, 16384, 8, 3, "mixed"),
+          # rows enough for the wide kernel of ranks above 32, in each direction
+          (4100, 136, 4104, 64, 3, "requests"), (4111, 4120, 136, 100, 2, "mixed"), (4200, 72, 4096, 33, 4, "own"),
+          # every size of cluster of the few-token kernel, one adapter or many
+          (2, 5120, 72, 64, 1024, "own"), (40, 2048, 2048, 16, 2, "mixed"), (200, 1024, 1024, 40, 64, "mixed"),
+          (1000, 256, 256, 8, 500, "own"), (255, 8, 8, 4, 3, "mixed"), (256, 8, 8, 4, 3, "mixed"),
+          # uneven adapters over many column blocks
+          (1500, 2048, 1536, 16, 17, "requests"), (900, 640, 640, 8, 56, "mixed")]
 
 
 @pytest.mark.parametrize("T,K,N,R,n,kind", SHAPES)
@@ -315,13 +322,51 @@ def test_repeatable_streams_graph():
         _close(out[has], want[has], tol[has] + 1e-37, "out")
 
 
+@pytest.mark.parametrize("T,n", [(61, 7), (500, 3)])
+def test_two_calls_at_once(T, n):
+    """Two batches on two streams side by side, each with buffers of its own,
+    give the bits of one after the other."""
+    cs = [_case(T, 1024, 512, 24, n, "mixed", seed=s) for s in (1, 2)]
+    want = []
+    for c in cs:
+        v, out, _ = _forward(c)
+        want.append((v, out, *_backward(c, v)))
+    streams = [torch.cuda.Stream() for _ in cs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(3):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(s):
+                v, out, _ = _forward(c)
+                got[i] = (v, out, *_backward(c, v))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for p, q in zip(got[i], want[i]):
+            assert torch.equal(p, q)
+
+
+def test_first_use_inside_a_capture():
+    """A graph may capture the first call of a shape: nothing in a call
+    allocates, synchronises or runs on another stream."""
+    c = _case(4500, 72, 4096, 72, 2, "requests", seed=12)
+    v, out = torch.zeros((4500, 72), device="cuda"), c["base"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fm.moe_lora(c["x"], c["a"], c["b"], c["scales"], c["batch"].offsets, c["batch"].sorted, c["base"], v, out)
+    graph.replay()
+    has = c["ids"] >= 0
+    _, _, want, tol = _exact_forward(c, c["base"])
+    _close(out[has], want[has], tol[has] + 1e-37, "out")
+
+
 def test_binding_refusals():
     c = _case(20, 64, 32, 4, 2, "mixed")
     v, out = torch.empty((20, 4), device="cuda"), torch.empty((20, 32), device="cuda")
     b = c["batch"]
     good = dict(x=c["x"], lora_a=c["a"], lora_b=c["b"], scales=c["scales"], adapter_offsets=b.offsets,
                 sorted_tokens=b.sorted, base=c["base"], v=v, out=out)
-    for name, bad in (("x", c["x"].float()), ("x", c["x"].t()), ("lora_a", c["a"][:, :3]), ("lora_b", c["b"].float()),
+    for name, bad in (("x", c["x"].float()), ("x", c["x"].t()), ("out", out[:1].expand(20, 32)), ("lora_a", c["a"][:, :3]), ("lora_b", c["b"].float()),
                       ("scales", c["scales"].double()), ("adapter_offsets", b.offsets[:2]),
                       ("sorted_tokens", b.sorted.long()), ("base", c["base"][:, :31]), ("v", v[:19]),
                       ("out", out.cpu()), ("out_bf16", out)):
