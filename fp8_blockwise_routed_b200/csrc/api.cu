@@ -497,7 +497,8 @@ int moe_lora(const uint16_t* x, int64_t ld_x, int64_t T, int K, const uint16_t* 
     p.out = out;
     p.ld_out = ld_out;
     p.out_bf16 = out_bf16;
-    cudaError_t err = launch_lora(rows, rank, p, s);
+    bool two = false;
+    cudaError_t err = launch_lora(rows, rank, p, &two, s);
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_lora");
 }
 
@@ -551,10 +552,11 @@ int moe_lora_backward(const uint16_t* x, int64_t ld_x, int64_t T, int K, const u
         p.out = dx;
         p.ld_out = ld_dx;
     }
-    cudaError_t err = T > 0 ? launch_lora(rows, rank, p, s) : cudaSuccess;
+    bool two = false;
+    cudaError_t err = T > 0 ? launch_lora(rows, rank, p, &two, s) : cudaSuccess;
     if (err == cudaSuccess)
         err = launch_lora_outer(rows, rank, LoraOuter{dv_terms, x, ld_x, K, nullptr, d_a},
-                                LoraOuter{v_terms, dout, ld_dout, N, scales, d_b}, s);
+                                LoraOuter{v_terms, dout, ld_dout, N, scales, d_b}, two, s);
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_lora_backward");
 }
 

@@ -261,7 +261,9 @@ struct LoraProduct {
     uint16_t* out_bf16;
 };
 size_t lora_terms_bytes(int64_t T, int R);
-cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, cudaStream_t s);
+// *two_kernels: whether v and out were left to two kernels (then the last one
+// started no dependent launch before v was complete).
+cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, bool* two_kernels, cudaStream_t s);
 // d[a, r, c] = f_a * sum_p v[p, r] x[tok(p), c], two such products at once
 struct LoraOuter {
     const uint16_t* v_terms;
@@ -271,6 +273,8 @@ struct LoraOuter {
     const float* scales;
     float* d;
 };
-cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, const LoraOuter& b, cudaStream_t s);
+// behind_expand: *two_kernels of the launch_lora before it.
+cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, const LoraOuter& b, bool behind_expand,
+                              cudaStream_t s);
 
 }  // namespace fp8moe

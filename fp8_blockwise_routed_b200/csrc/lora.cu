@@ -126,8 +126,11 @@ __device__ __forceinline__ void tmem_ld16x256_x4(uint32_t taddr, uint32_t (&r)[1
 }
 
 // Programmatic launch: a kernel of a call lets the next one start its blocks
-// (which load what does not depend on it) and that one waits here until
-// everything before it in the stream is complete and visible.
+// (which load what does not depend on it) and that one waits until everything
+// before it in the stream is complete and visible.  The expand lets the next
+// kernel start only once its own wait is over, so the outer product behind it
+// starts with the shrink complete: it needs nothing of the expand, runs beside
+// its end, and waits for it before its own.
 __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -784,7 +787,6 @@ __global__ void __launch_bounds__(kExpandThreads)
     extern __shared__ __align__(16) uint8_t dyn[];
     uint32_t* const frag = reinterpret_cast<uint32_t*>(dyn);  // [BT / 16][3][KS][32 * 4]
     __shared__ int s_tok[BT];
-    allow_next();
     const Tile tile = find_tile<kExpandThreads>(rows, BT, blockIdx.x / cblocks);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, q = lane & 3;
@@ -843,6 +845,7 @@ __global__ void __launch_bounds__(kExpandThreads)
 #pragma unroll
     for (int i = 0; i < RING - 1; ++i) fetch(16 * i);
     wait_previous();  // v
+    allow_next();
     // the terms of v, four ranks of one token at a time, in the order of the A
     // operand: lane 4 g + q holds rows g, g + 8 and ranks 16 s + 4 q + 0..3
     {
@@ -982,7 +985,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     auto wait = [&](uint32_t b, uint32_t phase) {
         return sm100::mbar_wait_bounded(b, phase & 1, abort, kTileWaitNs);
     };
-    allow_next();
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
             sm100::mbar_init(bar(kBaseIn, b), 128);
@@ -1045,7 +1047,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         } else {
             if (warp < 8) {
                 // the terms of v: row tid % 128, every other 8 ranks
-                if (!waited) wait_previous();
+                if (!waited) {
+                    wait_previous();
+                    allow_next();
+                }
                 waited = true;
                 const int row = tid & 127;
                 const bool in = row < tile.count;
@@ -1276,7 +1281,8 @@ __device__ __forceinline__ OuterItem outer_item(const LoraRows& rows, const int1
 
 __global__ void __launch_bounds__(kOuterThreads, 2)
     lora_outer_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      LoraRows rows, int R, int rblocks, OuterSide pa, OuterSide pb, int ablocks, int blocks)
+                      LoraRows rows, int R, int rblocks, OuterSide pa, OuterSide pb, int ablocks, int blocks,
+                      bool behind_expand)
 {
     constexpr int S = kOuterStages;
     extern __shared__ uint8_t dyn[];
@@ -1427,7 +1433,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
                         cp_async16(at + j * kOuterPanel + (row0 + 16 * h) * 128 + swz, in ? src + j * 64 : px, in);
                     }
                 }
-                if (!waited) wait_previous();  // the terms of dv
+                if (!waited && !behind_expand) wait_previous();  // the terms of dv
                 waited = true;
                 if (p + kOuterTokens <= o.hi) {
                     if (pt == 0) {
@@ -1645,8 +1651,9 @@ Terms terms_at(uint16_t* at, int64_t T, int R) { return Terms{at, T * round8(R),
 
 size_t lora_terms_bytes(int64_t T, int R) { return static_cast<size_t>(T) * round8(R) * 3 * 2; }
 
-cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, cudaStream_t s)
+cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, bool* two_kernels, cudaStream_t s)
 {
+    *two_kernels = false;
     DeviceInfo di;
     if (!device_info(&di)) return cudaErrorUnknown;
     const Terms t = terms_at(p.v_terms, rows.T, R), ut = terms_at(p.u_terms, rows.T, R);
@@ -1669,6 +1676,7 @@ cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, cudaS
     else
         err = shrink_tile<128>(rows, p.x, p.ldx, p.C1, p.w1, R, p.f1, p.v, t, p.u, ut, sms, s);
     if (err != cudaSuccess || !p.w2) return err;
+    *two_kernels = true;
     // Ranks above 32 with many tokens per adapter and enough rows to fill the
     // GPU: the tcgen05 kernel (16384 x 6144, rank 64: 164 us against 220;
     // 4096 x 5120: 48 against 64; 2048 x 2048: 28 against 25).  Up to rank
@@ -1688,7 +1696,8 @@ cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, cudaS
     return expand<8, 4, 32, 3>(rows, p.v, R, p.w2, p.C2, p.f2, p.base, p.ld_base, p.out, p.ld_out, p.out_bf16, s);
 }
 
-cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, const LoraOuter& b, cudaStream_t s)
+cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, const LoraOuter& b, bool behind_expand,
+                              cudaStream_t s)
 {
     const int rblocks = (R + kOuterRanks - 1) / kOuterRanks;
     const int ab = (a.C + kOuterCols - 1) / kOuterCols, bb = (b.C + kOuterCols - 1) / kOuterCols;
@@ -1722,7 +1731,7 @@ cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, c
     if (err != cudaSuccess) return err;
     Launch l(grid, kOuterThreads, kOuterSmem, s, nc, true);
     return cudaLaunchKernelEx(&l.cfg, lora_outer_kernel, map[0], map[1], rows, R, rblocks, side[0], side[1], ab,
-                              ab + bb);
+                              ab + bb, behind_expand);
 }
 
 }  // namespace fp8moe
