@@ -509,7 +509,7 @@ constexpr int kTileThreads = 288;  // four warps of sums, four producers, the is
 constexpr int kTileChain = 4;      // stages per accumulation chain
 constexpr uint64_t kTileWaitNs = 2000000000ull;
 
-constexpr int tile_stages(int RP) { return RP <= 64 ? 4 : 6; }
+constexpr int tile_stages(int RP) { return RP <= 32 ? 5 : RP <= 64 ? 4 : 6; }
 constexpr int tile_blocks(int RP) { return RP <= 64 ? 2 : 1; }  // per SM
 constexpr int tile_stage_bytes(int RP) { return (kTileTokens + RP) * 128; }
 constexpr int tile_smem(int RP) { return 1024 + tile_stages(RP) * tile_stage_bytes(RP); }
@@ -1548,7 +1548,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
     cluster.sync();  // the peers have read this block's sums
 }
 
-// A launch with up to two attributes: cluster size along x (0: none), and
+// A launch with up to two attributes: cluster size along x, and
 // programmatic launch after the kernel before it.
 struct Launch {
     cudaLaunchConfig_t cfg{};
@@ -1560,7 +1560,7 @@ struct Launch {
         cfg.dynamicSmemBytes = smem;
         cfg.stream = s;
         cfg.attrs = at;
-        if (cluster) {
+        if (cluster > 1) {  // (a cluster of one needs none, and launches faster)
             at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
             at[cfg.numAttrs].val.clusterDim.x = cluster;
             at[cfg.numAttrs].val.clusterDim.y = 1;
@@ -1659,7 +1659,12 @@ cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, bool*
     const Terms t = terms_at(p.v_terms, rows.T, R), ut = terms_at(p.u_terms, rows.T, R);
     const int sms = di.sm_count;
     // Few tokens, or few for each adapter: one launch over tiles of 8 tokens.
-    if (rows.T < 256 || rows.T < 16 * static_cast<int64_t>(rows.n)) {
+    // Measured, this one / the two kernels: 256 tokens on 16 adapters of rank 64,
+    // 2048 to 2048, 11 / 15 us; 400 on 4, 5120 to 1536, 14 / 16.5; 512 on one,
+    // 5120 to 5120, 23 / 19.5, of rank 32 on six 16 / 18; 4096 on 256 of rank 16,
+    // 2048 to 2048, 31.5 / 41.5; 2048 on 200 of rank 64, 5120 to 5120, 128 / 113
+    // (two tiles of 8 tokens each read an adapter's ranks).
+    if (rows.T <= (R <= 32 ? 512 : 384) || rows.T < (R <= 32 ? 24 : 8) * static_cast<int64_t>(rows.n)) {
         const SmallArgs a{p.x,    p.ldx, p.C1,   p.w1,      p.f1,  p.v,      t,         p.u, ut, p.w2,
                           p.C2, p.f2,  p.base, p.ld_base, p.out, p.ld_out, p.out_bf16};
         if (R <= 16) return small<1>(rows, R, a, sms, s);
@@ -1677,11 +1682,12 @@ cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, bool*
         err = shrink_tile<128>(rows, p.x, p.ldx, p.C1, p.w1, R, p.f1, p.v, t, p.u, ut, sms, s);
     if (err != cudaSuccess || !p.w2) return err;
     *two_kernels = true;
-    // Ranks above 32 with many tokens per adapter and enough rows to fill the
-    // GPU: the tcgen05 kernel (16384 x 6144, rank 64: 164 us against 220;
-    // 4096 x 5120: 48 against 64; 2048 x 2048: 28 against 25).  Up to rank
-    // 32 the register kernel is ahead (rank 16: 136 us against 153).
-    if (R > 32 && rows.T >= 64 * static_cast<int64_t>(rows.n) && rows.T * p.C2 >= (int64_t(1) << 24)) {
+    // Ranks above 32 with many tokens per adapter and rows enough to fill the
+    // GPU: the tcgen05 kernel.  Both measured, rank 64, register kernel / this
+    // one: 16384 x 6144 220 / 164 us, 4096 x 5120 64 / 48, 2000 x 5120 36 / 35,
+    // 2048 x 2048 20 / 23; 4096 x 5120 with 32 tokens per adapter 76 / 102.  Up
+    // to rank 32 the register kernel is ahead (16384 x 6144, rank 16: 136 / 153).
+    if (R > 32 && rows.T >= 64 * static_cast<int64_t>(rows.n) && rows.T * p.C2 >= (int64_t(1) << 23)) {
         if (R <= 64)
             return expand_tile<64>(rows, p.v, R, p.w2, p.C2, p.f2, p.base, p.ld_base, p.out, p.ld_out, p.out_bf16, sms,
                                    s);

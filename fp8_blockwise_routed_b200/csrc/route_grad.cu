@@ -790,6 +790,7 @@ cudaError_t balance(const float* logits, int64_t T, int E, const int32_t* offset
         unsigned nc = 1;  // blocks with four rows per warp or more
         while (nc < kSmallBlocks && T > static_cast<int64_t>(nc) * kLossWarps * 4 * (32 / LPR)) nc *= 2;
         at[0].val.clusterDim.x = nc;
+        cfg.numAttrs = nc > 1 ? 1 : 0;  // (a cluster of one needs none, and launches faster)
         cfg.gridDim = dim3(nc);
         return cudaLaunchKernelEx(&cfg, balance_small_kernel<VPL, LPR>, logits, T, E, offsets, loss, counts, prob_mean);
     }

@@ -115,7 +115,10 @@ SHAPES = [(1, 8, 8, 1, 1, "one"), (1, 5120, 640, 16, 8, "one"), (5, 24, 40, 3, 2
           (2, 5120, 72, 64, 1024, "own"), (40, 2048, 2048, 16, 2, "mixed"), (200, 1024, 1024, 40, 64, "mixed"),
           (1000, 256, 256, 8, 500, "own"), (255, 8, 8, 4, 3, "mixed"), (256, 8, 8, 4, 3, "mixed"),
           # uneven adapters over many column blocks
-          (1500, 2048, 1536, 16, 17, "requests"), (900, 640, 640, 8, 56, "mixed")]
+          (1500, 2048, 1536, 16, 17, "requests"), (900, 640, 640, 8, 56, "mixed"),
+          # ranks that are no multiple of four, or above 64, behind the tiled first product
+          (900, 264, 520, 13, 5, "mixed"), (600, 264, 520, 100, 2, "requests"), (520, 72, 2056, 127, 1, "one"),
+          (385, 512, 512, 64, 48, "mixed"), (513, 512, 512, 32, 21, "mixed")]
 
 
 @pytest.mark.parametrize("T,K,N,R,n,kind", SHAPES)
@@ -287,11 +290,14 @@ def test_entries_outside_the_batch_are_skipped():
     assert torch.equal(out2[keep], out[keep]) and bool((out2[lost] == -7.0).all())
 
 
-def test_repeatable_streams_graph():
-    c = _case(333, 520, 264, 24, 6, "requests", seed=8)
-    ad = LoraAdapters(c["a"], c["b"], c["scales"], 400)
-    batch = LoraBatch(6, 400)
-    out, gx = c["base"].clone(), torch.zeros((333, 520), device="cuda")
+@pytest.mark.parametrize("T", [333, 1333])
+def test_repeatable_streams_graph(T):
+    """Another batch in the same buffers, replayed from a graph and run on another
+    stream: the same bits, and right."""
+    c = _case(T, 520, 264, 24, 6, "requests", seed=8)
+    ad = LoraAdapters(c["a"], c["b"], c["scales"], 1400)
+    batch = LoraBatch(6, 1400)
+    out, gx = c["base"].clone(), torch.zeros((T, 520), device="cuda")
     graph = torch.cuda.CUDAGraph()
     ids, x = c["ids"].clone(), c["x"].clone()
     ad.backward(batch.assign(ids), x, c["dout"], None, gx)   # buffers exist before the capture
@@ -300,8 +306,8 @@ def test_repeatable_streams_graph():
         ad.forward(batch, x, c["base"], out)
         g_a, g_b = ad.backward(batch, x, c["dout"], None, gx)
     for seed in (1, 2):
-        ids.copy_(torch.from_numpy(_ids(333, 6, "mixed", seed).astype(np.int32)))
-        x.copy_(torch.randn((333, 520), device="cuda"))
+        ids.copy_(torch.from_numpy(_ids(T, 6, "mixed", seed).astype(np.int32)))
+        x.copy_(torch.randn((T, 520), device="cuda"))
         out.copy_(c["base"])
         gx.zero_()
         graph.replay()
@@ -322,7 +328,7 @@ def test_repeatable_streams_graph():
         _close(out[has], want[has], tol[has] + 1e-37, "out")
 
 
-@pytest.mark.parametrize("T,n", [(61, 7), (500, 3)])
+@pytest.mark.parametrize("T,n", [(61, 7), (500, 3), (900, 3)])
 def test_two_calls_at_once(T, n):
     """Two batches on two streams side by side, each with buffers of its own,
     give the bits of one after the other."""
