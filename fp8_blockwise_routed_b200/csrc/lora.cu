@@ -10,8 +10,10 @@
 //   dv_p  = f_a B_a dout_t                  (shrink)
 //   dx_t  = dx_base_t + A_a^T dv_p          (expand)
 //   dA_a  = sum_p dv_p x_t^T,  dB_a = f_a sum_p v_p dout_t^T   (outer)
-// so three kernels carry both directions; the rank-major B is what makes the
-// backward shrink and expand the same products as the forward ones.
+// so three products carry both directions; the rank-major B is what makes the
+// backward shrink and expand the same as the forward ones.  Few tokens take
+// shrink and expand in one launch (lora_small_kernel), many a kernel for each
+// (launch_lora has the rule).
 //
 // Precision: x, dout, A and B are BF16 and their products exact in FP32; v
 // and dv stay FP32.  Where v or dv meets the tensor cores it is split into
@@ -490,20 +492,19 @@ __global__ void __launch_bounds__(kSmallThreads, 2) lora_small_kernel(LoraRows r
 // ------------------------------------------------------------------ shrink
 //
 // v[p, r] = f_a sum_c x[tok, c] w[a, r, c] for adapters with many tokens: 128
-// tokens times all ranks per cluster on tcgen05, the columns dealt to the cluster's blocks 64 at a
-// time.  A stage holds the 128 token rows and the RP rank rows of 64 columns
+// tokens times all ranks per cluster on tcgen05, the columns dealt to the
+// cluster's blocks 64 at a time.  A stage holds the 128 token rows and the RP rank rows of 64 columns
 // (128-byte rows, 128-byte swizzle); four producer warps bring in the token
 // rows by cp.async, which gathers them and zero-fills what is missing, one TMA
 // box the rank rows (cp.async sustains about 40 bytes per clock and SM, which
-// these rows would share), and one thread issues the four MMAs.  Four more warps move the accumulator to FP32
-// registers every four stages (two TMEM buffers in turn), so a chain on the
-// tensor core stays 256 columns long (unbroken, 16384 columns come out 2e-6
+// these rows would share), and one thread issues the four MMAs.  Four more
+// warps move the accumulator to FP32 registers every four stages (two TMEM
+// buffers in turn), so a chain on the tensor core stays 256 columns long (unbroken, 16384 columns come out 2e-6
 // off; so, 2.4e-7).  The producers neither fence nor read TMEM: both wait for
 // a thread's copies in flight, which kept one stage in flight instead of S
-// (16384 x 6144, rank 64: 72 us against 51, with the
-// launch behind it).  The proxy fence is the
-// issuer's, behind the barrier that the copies arrive on.  At the end the
-// blocks' sums are joined in block order.
+// (16384 x 6144, rank 64: 72 us against 48, 4.3 TB/s of x and A).  The proxy
+// fence is the issuer's, behind the barrier that the copies arrive on.  At the
+// end the blocks' sums are joined in block order.
 constexpr int kTileTokens = 128;
 constexpr int kTileThreads = 288;  // four warps of sums, four producers, the issuer
 constexpr int kTileChain = 4;      // stages per accumulation chain
@@ -943,7 +944,7 @@ __global__ void __launch_bounds__(kExpandThreads)
 // MN-major, by TMA, used once per term.  Base rows come in by cp.async; a
 // thread of the epilogue owns one row (TMEM lane), forms its sums in place, and
 // its warp writes the rows out whole.  (One bulk copy per row and direction
-// instead: 206 us against 172 us for 16384 x 6144, rank 64; the copy engine
+// instead: 206 us against 164 us for 16384 x 6144, rank 64; the copy engine
 // takes a request about every 32 clocks, whatever its size.)  Two
 // row buffers, each with its own four epilogue warps, take turns; the products
 // run up to four blocks ahead of them (four accumulators in TMEM, two slabs),
@@ -1222,8 +1223,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // kOuterChain stages (two TMEM buffers in turn), so no long sum is left to the
 // tensor core's rounding, and write an item out.  Blocks are persistent, two
 // per SM, and the ring runs on from item to item: an item is a few stages,
-// shorter than a block's start and end (one item per block: 149 us for the
-// whole GLM-sized gradient against 111).  Items go from the adapter with most
+// shorter than a block's start and end (one item per block: the whole
+// gradient of 4096 x 5120, rank 64, 16 adapters took 38 us more).  Items go from the adapter with most
 // tokens to the one with fewest, dealt to the blocks there and back, so that
 // uneven adapters even out.  With few adapters there are too few items for
 // that; then the blocks of a cluster share one item's tokens and join their
