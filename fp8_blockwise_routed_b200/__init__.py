@@ -173,6 +173,8 @@ def _refuse(what: str, detail: str):
 
 
 def _refuse_arg(what: str, name: str, t, dtype, shape, dev: int, how: str):
+    if t is None:
+        _refuse(what, f"{name} is missing")
     if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or t.get_device() == dev:
         _refuse(what, f"{name}: expected {dtype} {tuple(shape)} with {how}, got {t.dtype} {tuple(t.shape)}"
                       f" with strides {t.stride()}")
@@ -185,14 +187,14 @@ def _refuse_arg(what: str, name: str, t, dtype, shape, dev: int, how: str):
 def _arg(what: str, name: str, t, dtype, shape, dev: int):
     """Address of a contiguous tensor after checking its type, shape and
     device (dev: a CUDA device index)."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+    if t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
         return t.data_ptr()
     _refuse_arg(what, name, t, dtype, shape, dev, "contiguous elements")
 
 
 def _rows(what: str, name: str, t, dtype, T: int, C: int, dev: int):
     """Address and row stride of a [T, C] tensor whose rows are contiguous."""
-    if t.dtype is dtype and t.shape == (T, C) and t.get_device() == dev:
+    if t is not None and t.dtype is dtype and t.shape == (T, C) and t.get_device() == dev:
         if t.is_contiguous():
             return t.data_ptr(), C
         ld, one = t.stride()
@@ -731,10 +733,11 @@ class RoutedMoE(_RouterGradient):
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, out_bf16: torch.Tensor | None = None,
                 stream=None, stage_events=None, fused: bool = True, adapters=None, batch=None) -> torch.Tensor:
-        """adapters, batch: a LoraAdapters (H to H) and the LoraBatch of
-        these tokens, whose rows are added to the layer's.  stage_events: None, or 7 recorded torch.cuda.Events marking the
+        """stage_events: None, or 7 recorded torch.cuda.Events marking the
         start of quantise, route, gather, gate/up, down, combine and the end
-        (fused: the first two both mark the start of moe_route_quant)."""
+        (fused: the first two both mark the start of moe_route_quant).
+        adapters, batch: a LoraAdapters (H to H) and the LoraBatch of these
+        tokens, whose rows are added to the layer's."""
         T = x.shape[0]
         assert T <= self.max_tokens and x.shape[1] == self.H and logits.shape == (T, self.E)
         codes, scales = self.codes[:T], self.scales[:T]
@@ -799,8 +802,9 @@ class RoutedMoEMX(_RouterGradient):
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, out_bf16: torch.Tensor | None = None,
                 stream=None, stage_events=None, adapters=None, batch=None) -> torch.Tensor:
-        """adapters, batch: as RoutedMoE.forward.  stage_events: None, or 6 recorded torch.cuda.Events marking the
-        start of quantise + route, gather, gate/up, down, combine and the end."""
+        """stage_events: None, or 6 recorded torch.cuda.Events marking the
+        start of quantise + route, gather, gate/up, down, combine and the end.
+        adapters, batch: as RoutedMoE.forward."""
         T = x.shape[0]
         assert T <= self.max_tokens and x.shape[1] == self.H and logits.shape == (T, self.E)
         codes, scales = self.codes[:T], self.scales[:T]

@@ -702,6 +702,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
         __syncwarp();
     }
     __syncthreads();  // every chain is read: the MMAs and the ring are done with
+    if (s_abort) sm100::settle();
     if (warp == 8) {
         sm100::tc_fence_after();
         sm100::tmem_dealloc(tmem, tile_tmem(RP));
@@ -1504,6 +1505,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
     }
     __syncwarp();
     __syncthreads();  // every chain is read: the MMAs and the ring are done with
+    if (s_abort) sm100::settle();
     wait_previous();  // (blocks without a stage) never end before the kernel they follow
     if (warp == 8) {
         sm100::tc_fence_after();

@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(kLossWarps * 32)
     if (!ok) sums.z = NAN;  // a wait that ran out
     const LossSums own = join_warps<VPL, LPR>(sums, E, s_sum);
     write_part<VPL, LPR>(own, s_sum, E, part, part_z, part_n);
+    if (s_abort) sm100::settle();
 }
 
 // ... summed by one cluster of eight blocks, which share the experts; the
@@ -740,6 +741,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             grad_row<VPL, 32>(v, g, zc, E, k, id, s - wj * total, d_logits + t * E, lane, true);
         }
     }
+    __syncthreads();
+    if (s_abort) sm100::settle();
 }
 
 // Without slot rows: the balance and z gradients alone, 32 / LPR rows per warp.

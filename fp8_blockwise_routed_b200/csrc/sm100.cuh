@@ -117,6 +117,14 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
+// After a wait that ran out: a pause (1 ms, bounded) in which the copies that
+// are still in flight land before the block's shared memory is given back.
+__device__ __forceinline__ void settle()
+{
+    const uint64_t t0 = global_timer_ns();
+    for (int i = 0; i < 65536 && global_timer_ns() - t0 < 1000000ull; ++i) __nanosleep(500);
+}
+
 // ---------------------------------------------------------------- registers
 // Per-warpgroup register budget (all four warps of a warpgroup execute it).
 template <uint32_t N>

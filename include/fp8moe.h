@@ -564,7 +564,8 @@ MOE_API int moe_route_backward(const float* logits, int64_t T, int E, const int3
  * K, N multiples of 8, 8 .. 16384; ld_x a multiple of 8, ld_base and ld_out
  * of 4.  No workspace, no device status; v and out overlap nothing that is
  * read (but base).  One to two launches, two or three with the backward call;
- * a wait inside a kernel that expires leaves NaN in the rows concerned.
+ * a wait inside a kernel that expires leaves NaN in the rows concerned.  An
+ * element of v or dv within 2^-9 of FP32's largest counts as infinite.
  *
  * moe_lora_backward -- its gradients, for dout the gradient of out:
  *   dv[p, r]     = scales[a] * sum_c dout[t, c] lora_b[a, r, c]

@@ -379,6 +379,10 @@ def test_binding_refusals():
         with pytest.raises(fm.MoeError) as e:
             fm.moe_lora(**dict(good, **{name: bad}))
         assert e.value.code == 1 and name in str(e.value)
+    for name in ("lora_a", "adapter_offsets", "sorted_tokens", "v", "out"):
+        with pytest.raises(fm.MoeError) as e:
+            fm.moe_lora(**dict(good, **{name: None}))
+        assert e.value.code == 1 and f"{name} is missing" in str(e.value)
     with pytest.raises(fm.MoeError) as e:   # rows that start off a 16-byte boundary
         fm.moe_lora(**dict(good, base=torch.zeros((20, 33), device="cuda")[:, 1:]))
     assert e.value.code in (1, 3)
@@ -387,6 +391,29 @@ def test_binding_refusals():
         fm.moe_lora_backward(c["x"], c["a"], c["b"], None, b.offsets, b.sorted, v, c["dout"], None, None, d_a, d_b,
                              torch.empty((16,), dtype=torch.uint8, device="cuda"))
     assert e.value.code == 4
+
+
+def test_infinite_rows_stay_infinite():
+    """An infinite x gives infinite or NaN elements where the formula does, in
+    its own row only, on the few-token and the tiled paths."""
+    for T, R in ((20, 8), (900, 64)):
+        c = _case(T, 64, 32, R, 2, "mixed")
+        c["x"][3, 5] = float("inf")
+        v, out = torch.empty((T, R), device="cuda"), c["base"].clone()
+        b = c["batch"]
+        fm.moe_lora(c["x"], c["a"], c["b"], c["scales"], b.offsets, b.sorted, c["base"], v, out)
+        clean = c["x"].clone()
+        clean[3] = 0
+        v2, out2 = torch.empty((T, R), device="cuda"), c["base"].clone()
+        fm.moe_lora(clean, c["a"], c["b"], c["scales"], b.offsets, b.sorted, c["base"], v2, out2)
+        rest = torch.arange(T, device="cuda") != 3
+        assert torch.equal(out[rest], out2[rest])
+        a = int(c["ids"][3])
+        if a >= 0:
+            want = (c["x"][3].double() @ c["a"][a].double().t()) @ c["b"][a].double() * float(
+                1 if c["scales"] is None else c["scales"][a]) + c["base"][3].double()
+            assert not want.isfinite().any()
+            assert torch.equal(out[3].isnan(), want.isnan()) and torch.equal(out[3].isposinf(), want.isposinf())
 
 
 @pytest.mark.parametrize("mx", [False, True])
