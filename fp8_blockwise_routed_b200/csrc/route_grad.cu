@@ -32,6 +32,10 @@ namespace {
 __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The two halves of a cluster barrier.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // A row of E <= VPL * LPR logits in the registers of LPR lanes: register i of
 // lane l holds expert 4 (l % LPR) + 4 LPR (i / 4) + i % 4, so that a lane's
 // four neighbours are one 16-byte access where E is a multiple of four.
@@ -460,6 +464,7 @@ __global__ void __launch_bounds__(kFinalThreads)
     __shared__ double s_red[kLossWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
+    cluster_arrive();  // this block has started: waited for before a peer's memory is written
     const int share = (E + kFinalBlocks - 1) / kFinalBlocks;  // at most 128 experts a block
     int width = 1;                                            // experts side by side, a power of two
     while (width < share) width *= 2;
@@ -494,6 +499,8 @@ __global__ void __launch_bounds__(kFinalThreads)
         counts[e] = c;
     }
     term = block_sum(term, s_red);
+    __syncwarp();
+    cluster_wait();  // every block of the cluster has started
     if (threadIdx.x == 0) cluster.map_shared_rank(s_term, 0)[rank] = term;
     cluster.sync();
     if (rank == 0 && threadIdx.x == 0) {

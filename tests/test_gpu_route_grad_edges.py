@@ -1,0 +1,44 @@
+"""moe_balance_loss and moe_route_backward at the edges of their ranges and
+beside other work."""
+import pytest
+import torch
+
+import fp8_blockwise_routed_b200 as fm
+
+pytestmark = pytest.mark.gpu
+
+
+def _offsets(T, E, k):
+    """Offsets of T * k pairs spread over the experts."""
+    return torch.div(torch.arange(E + 1, device="cuda") * T * k, E, rounding_mode="floor").to(torch.int32)
+
+
+def _loss_buffers(T, E):
+    return (torch.full((2,), -7.0, device="cuda"), torch.full((E + 1,), -7, dtype=torch.int32, device="cuda"),
+            torch.full((E,), -7.0, device="cuda"),
+            torch.full((fm.moe_balance_loss_workspace_bytes(T, E),), 255, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("T,E", [(4096, 256), (3001, 257), (66667, 4)])
+def test_blocks_that_start_apart_join_alike(T, E):
+    """The blocks that join the partial sums get their SMs one by one when
+    another stream keeps the GPU busy; the losses keep their bits."""
+    z = torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    off = _offsets(T, E, 2)
+    want = _loss_buffers(T, E)
+    fm.moe_balance_loss(z, off, *want)
+    assert torch.isfinite(want[0]).all()
+    busy = torch.cuda.Stream()
+    work = torch.randn((1 << 24,), device="cuda")
+    m = torch.randn((2048, 2048), device="cuda")
+    busy.wait_stream(torch.cuda.current_stream())
+    got = [_loss_buffers(T, E) for _ in range(40)]
+    for i, g in enumerate(got):
+        with torch.cuda.stream(busy):
+            work.mul_(1.0)
+            torch.mm(m, m)
+        fm.moe_balance_loss(z, off, *g)
+    torch.cuda.synchronize()
+    for g in got:
+        for p, q in zip(g[:3], want[:3]):
+            assert torch.equal(p, q)
