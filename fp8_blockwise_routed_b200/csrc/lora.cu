@@ -1738,7 +1738,10 @@ cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, c
     }
     cudaError_t err = allow_smem<lora_outer_kernel>(kOuterSmem);
     if (err != cudaSuccess) return err;
-    Launch l(grid, kOuterThreads, kOuterSmem, s, nc, true);
+    // Without tokens no kernel of this call runs before this one, and the one
+    // before it in the stream may be the expand of another call, which lets a
+    // programmatic launch start while it still writes.
+    Launch l(grid, kOuterThreads, kOuterSmem, s, nc, rows.T > 0);
     return cudaLaunchKernelEx(&l.cfg, lora_outer_kernel, map[0], map[1], rows, R, rblocks, side[0], side[1], ab,
                               ab + bb, behind_expand);
 }
