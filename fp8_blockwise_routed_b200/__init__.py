@@ -142,6 +142,8 @@ def lib() -> ctypes.CDLL:
         L.moe_lora_backward.restype = i32
         L.moe_lora_backward.argtypes = [P, i64, i64, i32, P, P, P, i32, i32, i32, P, P, P, P, i64, P, i64, P, i64,
                                         P, P, P, sz, P]
+        L.moe_debug_waits.restype = None
+        L.moe_debug_waits.argtypes = [ctypes.c_uint64, ctypes.c_uint32]
         L.moe_debug_grouped_down_mx.restype = i32
         L.moe_debug_grouped_down_mx.argtypes = [P, P, i64, i32, i32, P, P, P, i32, i32, P, P, P, P, sz, P]
         _lib = L
@@ -385,6 +387,12 @@ def moe_get_device_status(ws) -> int:
 
 def moe_debug_encode(inp, out, stream=None):
     _check(lib().moe_debug_encode(_p(inp), inp.numel(), _p(out), _s(stream)), "moe_debug_encode")
+
+
+def moe_debug_waits(wait_ns: int = 0, held: int = 0):
+    """Test hook: limit of the waits inside the kernels (0: 2 s) and the mask
+    of barriers held open, for every launch after it; see the header."""
+    lib().moe_debug_waits(wait_ns, held)
 
 
 def moe_ffn_intermediate(ws, T: int, H: int, I: int, top_k: int):

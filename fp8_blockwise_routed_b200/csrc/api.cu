@@ -7,6 +7,7 @@
 // rejected call enqueues nothing.  Device-side faults are recorded in the
 // status word at the start of the call's workspace, which the call clears
 // (an async memset) before its first kernel.
+#include <atomic>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -44,6 +45,16 @@ bool device_info(DeviceInfo* out)
     }
     *out = d;
     return true;
+}
+
+// The kernels' wait limit and the barriers held open (moe_debug_waits).
+static constexpr uint64_t kWaitNs = 2000000000ull;
+static std::atomic<uint64_t> g_wait_ns{kWaitNs};
+static std::atomic<uint32_t> g_held{0};
+
+Waits waits()
+{
+    return Waits{g_wait_ns.load(std::memory_order_relaxed), g_held.load(std::memory_order_relaxed)};
 }
 
 }  // namespace fp8moe
@@ -558,6 +569,12 @@ int moe_lora_backward(const uint16_t* x, int64_t ld_x, int64_t T, int K, const u
         err = launch_lora_outer(rows, rank, LoraOuter{dv_terms, x, ld_x, K, nullptr, d_a},
                                 LoraOuter{v_terms, dout, ld_dout, N, scales, d_b}, two, s);
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_lora_backward");
+}
+
+void moe_debug_waits(uint64_t wait_ns, uint32_t held)
+{
+    g_wait_ns.store(wait_ns ? wait_ns : kWaitNs, std::memory_order_relaxed);
+    g_held.store(held, std::memory_order_relaxed);
 }
 
 int moe_get_device_status(const void* ws, int* status_out)

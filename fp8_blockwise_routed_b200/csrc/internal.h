@@ -203,6 +203,20 @@ size_t ffn_mx_workspace_layout(int64_t T, int H, int I, int k, size_t* off_a, si
                                size_t* off_sh);
 cudaError_t launch_grouped_ffn_mx(const FfnMxArgs& a, cudaStream_t s);
 
+// Bounded waits of the kernels below: their limit, and a mask of barriers that
+// expect one arrival that never comes (0 but in tests of what a wait leaves
+// that runs out).
+enum : uint32_t {
+    kHoldExpandSlab = 1u << 0,  // adapters, wide expand: rank rows in
+    kHoldExpandFree = 1u << 1,  // ... base row buffer free again
+};
+struct Waits {
+    uint64_t ns;
+    uint32_t held;
+    __host__ __device__ uint32_t extra(uint32_t barrier) const { return (held & barrier) ? 1u : 0u; }
+};
+Waits waits();
+
 // Balance loss: at most this many blocks sum the probabilities (one per SM of a
 // B200), so the partial sums and their order do not depend on T beyond it.
 constexpr int kLossMaxBlocks = 148;

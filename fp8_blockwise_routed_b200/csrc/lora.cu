@@ -964,7 +964,7 @@ template <int RP>
 __global__ void __launch_bounds__(kWideThreads, 1)
     lora_expand_tile_kernel(const __grid_constant__ CUtensorMap wmap, LoraRows rows, const float* v, int R, int C,
                             const float* __restrict__ scales, const float* base, int64_t ld_base, float* out,
-                            int64_t ld_out, uint16_t* __restrict__ out_bf16)
+                            int64_t ld_out, uint16_t* __restrict__ out_bf16, Waits waits)
 {
     constexpr int W = wide_cols(RP);
     constexpr int NP = wide_panels(RP);
@@ -985,13 +985,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     enum { kBaseIn = 0, kFree = 2, kSlabIn = 4, kSlabUsed = 6, kReady = 8, kRead = 12 };
     auto bar = [&](int kind, int i) { return sm100::smem_u32(&s_bar[kind + i]); };
     auto wait = [&](uint32_t b, uint32_t phase) {
-        return sm100::mbar_wait_bounded(b, phase & 1, abort, kTileWaitNs);
+        return sm100::mbar_wait_bounded(b, phase & 1, abort, waits.ns);
     };
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
             sm100::mbar_init(bar(kBaseIn, b), 128);
-            sm100::mbar_init(bar(kFree, b), 128);
-            sm100::mbar_init(bar(kSlabIn, b), 1);
+            sm100::mbar_init(bar(kFree, b), 128 + waits.extra(kHoldExpandFree));
+            sm100::mbar_init(bar(kSlabIn, b), 1 + waits.extra(kHoldExpandSlab));
             sm100::mbar_init(bar(kSlabUsed, b), 1);
         }
         for (int d = 0; d < 4; ++d) {
@@ -1034,8 +1034,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 const uint32_t u = use + j;
                 const int b = u & 1;
                 if (u >= 2) alive = wait(bar(kFree, b), (u >> 1) - 1);
+                if (!alive) break;  // the rows' barrier stays open, so the sums are not formed either
                 const int c = (b_lo + j) * W + pc;
-                if (base && alive && c < C) {
+                if (base && c < C) {
 #pragma unroll 8
                     for (int r = (warp - 9) * kAt + lane / (W / 4); r < kTileTokens; r += 4 * kAt) {
                         const int tok = s_tok[r];
@@ -1101,7 +1102,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     sm100::tma_load_3d(sm100::smem_u32(slabs + sl * kSlab + h * RP * 128), &wmap,
                                        ((b_lo + j) * W + 64 * h) * 2, 0, tile.a, bar(kSlabIn, sl));
             };
-            if (warp == 8) {  // the slabs of the tile before are all used
+            if (warp == 8 && alive) {  // the slabs of the tile before are all used
                 load_slab(0);
                 load_slab(1);
             }
@@ -1130,11 +1131,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     }
                     __syncwarp();
                     if (j > 0) {  // the slab before is free: fetch the one after this
-                        alive = wait(bar(kSlabUsed, sl ^ 1), (u - 1) >> 1);
-                        load_slab(j + 1);
+                        alive = __all_sync(0xFFFFFFFFu, wait(bar(kSlabUsed, sl ^ 1), (u - 1) >> 1));
+                        if (alive) load_slab(j + 1);
                     }
                 }
-                if (alive) alive = wait(bar(kSlabUsed, (use + nb - 1) & 1), (use + nb - 1) >> 1);
+                if (alive)
+                    alive = __all_sync(0xFFFFFFFFu, wait(bar(kSlabUsed, (use + nb - 1) & 1), (use + nb - 1) >> 1));
             } else {
                 const int b = warp >> 2;
                 const int row = tid & 127;
@@ -1148,12 +1150,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     const int d = u & 3;
                     alive = alive && wait(bar(kReady, d), u >> 2);
                     alive = alive && wait(bar(kBaseIn, b), u >> 1);
+                    // lanes may see a late arrival and the abort flag in either
+                    // order; what follows needs the whole warp
+                    alive = __all_sync(0xFFFFFFFFu, alive);
                     if (!alive) {  // a wait ran out: the row says so
                         if (tok >= 0)
-                            for (int c = 0; c < width; ++c) out[tok * ld_out + c0 + c] = NAN;
+                            for (int c = c0; c < c0 + width; ++c) {
+                                out[tok * ld_out + c] = NAN;
+                                if (out_bf16) out_bf16[static_cast<int64_t>(tok) * C + c] = 0x7FFF;
+                            }
                         continue;
                     }
-                    __syncwarp();
                     sm100::tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < W; c += 32) {
@@ -1196,15 +1203,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         it += nb;
     }
     if (!waited) wait_previous();  // this kernel never ends before the one it follows
-    // after a wait that ran out: copies in flight land before the block ends
     if (warp > 8) cp_async_wait_all();
-    if (warp == 8 && lane == 0 && s_abort) {
-        __shared__ int s_drain;
-        s_drain = 0;
-        for (int b = 0; b < 2; ++b)
-            sm100::mbar_wait_bounded(bar(kSlabIn, b), (((use + 1) >> 1) - 1) & 1, &s_drain, 1000000ull);
-    }
     __syncthreads();
+    if (s_abort) sm100::settle();
     if (warp == 8) {
         sm100::tc_fence_after();
         sm100::tmem_dealloc(tmem, 4 * W);
@@ -1629,7 +1630,7 @@ cudaError_t expand_tile(const LoraRows& rows, const float* v, int R, const uint1
     if (err != cudaSuccess) return err;
     Launch l(sm_count, kWideThreads, wide_smem(RP), s, 0, true);
     return cudaLaunchKernelEx(&l.cfg, lora_expand_tile_kernel<RP>, map, rows, v, R, C, scales, base, ld_base, out,
-                              ld_out, out_bf16);
+                              ld_out, out_bf16, waits());
 }
 
 template <int KS, int NW, int BT, int RING>

@@ -678,6 +678,14 @@ MOE_API int moe_debug_encode(const float* in, int64_t n, uint8_t* out, void* str
 MOE_API int moe_ffn_intermediate(const void* ws, int64_t T, int H, int I, int top_k,
                                  const uint8_t** h_codes, const float** h_scales);
 
+/* moe_debug_waits: makes the waits inside the kernels of moe_balance_loss,
+ * moe_route_backward, moe_lora and moe_lora_backward give up after wait_ns
+ * (0: the default, 2 s), and the barriers of the mask `held` (internal.h)
+ * expect one arrival that never comes, so that a test can see what a call
+ * leaves whose wait ran out.  For the whole process, from the next launch on;
+ * (0, 0) restores the defaults. */
+MOE_API void moe_debug_waits(uint64_t wait_ns, uint32_t held);
+
 /* moe_debug_grouped_down: the down GEMM of moe_grouped_ffn alone, on an
  * intermediate the caller supplies: h_codes [T*top_k, Ip] uint8 E4M3 and
  * h_scales [T*top_k, ceil(I/128)] FP32, rows in expert order (row r belongs

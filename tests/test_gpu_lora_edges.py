@@ -31,3 +31,51 @@ def test_gradient_without_tokens_waits_for_the_call_before(R):
         fm.moe_lora_backward(x[:0], a, b, None, none.offsets, none.sorted, v[:0], rnd(0, N), None, None, d_a, d_b, ws)
         assert not d_a.any() and not d_b.any()
         assert bool(out[T // 2].any())
+
+
+# barriers of moe_debug_waits
+EXPAND_SLAB, EXPAND_FREE = 1, 2
+LIMIT_NS = 50_000_000
+
+
+@pytest.fixture
+def held():
+    yield lambda mask: fm.moe_debug_waits(LIMIT_NS, mask)
+    torch.cuda.synchronize()
+    fm.moe_debug_waits(0, 0)
+
+
+@pytest.mark.parametrize("R", [64, 100])
+@pytest.mark.parametrize("barrier", [EXPAND_SLAB, EXPAND_FREE])
+def test_expand_whose_wait_runs_out(held, barrier, R):
+    """Where a wait of the wide expand runs out the rows' columns say so, in
+    FP32 and BF16; the others are right, and the next call is."""
+    T, K, N, n = 4200, 64, 4096, 2
+    g = torch.Generator(device="cuda").manual_seed(R)
+
+    def rnd(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    x, a, b = rnd(T, K), rnd(n, R, K), rnd(n, R, N)
+    base = torch.randn((T, N), generator=g, device="cuda")
+    batch = LoraBatch(n, T).assign(torch.arange(T, dtype=torch.int32, device="cuda") % n)
+
+    def forward():
+        v = torch.empty((T, R), device="cuda")
+        out, o16 = torch.full((T, N), -7.0, device="cuda"), torch.full((T, N), -7.0, device="cuda").to(torch.bfloat16)
+        fm.moe_lora(x, a, b, None, batch.offsets, batch.sorted, base, v, out, o16)
+        return v, out, o16
+
+    v, out, o16 = forward()
+    held(barrier)
+    v1, out1, o161 = forward()
+    torch.cuda.synchronize()
+    fm.moe_debug_waits(0, 0)
+    assert torch.equal(v1, v)                              # the first product has no part in it
+    gone = torch.isnan(out1)
+    assert torch.equal(torch.isnan(o161), gone) and bool(gone.any())
+    assert torch.equal(out1[~gone], out[~gone]) and torch.equal(o161[~gone], o16[~gone])
+    if barrier == EXPAND_SLAB:                             # no product without its rank rows
+        assert bool(gone.all())
+    for p, q in zip(forward(), (v, out, o16)):
+        assert torch.equal(p, q)
