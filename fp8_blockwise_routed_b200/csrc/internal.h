@@ -209,6 +209,8 @@ cudaError_t launch_grouped_ffn_mx(const FfnMxArgs& a, cudaStream_t s);
 enum : uint32_t {
     kHoldExpandSlab = 1u << 0,  // adapters, wide expand: rank rows in
     kHoldExpandFree = 1u << 1,  // ... base row buffer free again
+    kHoldShrinkFull = 1u << 2,  // adapters, tiled shrink: stage in
+    kHoldShrinkEmpty = 1u << 3, // ... stage used
 };
 struct Waits {
     uint64_t ns;

@@ -574,7 +574,7 @@ template <int RP>
 __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
     lora_shrink_tile_kernel(const __grid_constant__ CUtensorMap wmap, LoraRows rows, const uint16_t* __restrict__ x,
                             int64_t ldx, int C, int R, const float* __restrict__ scales, float* __restrict__ v,
-                            Terms terms, const float* __restrict__ u, Terms u_terms)
+                            Terms terms, const float* __restrict__ u, Terms u_terms, Waits waits)
 {
     constexpr int S = tile_stages(RP);
     constexpr int kStage = tile_stage_bytes(RP);
@@ -594,8 +594,9 @@ __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            sm100::mbar_init(sm100::smem_u32(&s_full[i]), 128 + 1);  // the copies of x, the box of w
-            sm100::mbar_init(sm100::smem_u32(&s_empty[i]), 1);
+            // the copies of x, the box of w
+            sm100::mbar_init(sm100::smem_u32(&s_full[i]), 128 + 1 + waits.extra(kHoldShrinkFull));
+            sm100::mbar_init(sm100::smem_u32(&s_empty[i]), 1 + waits.extra(kHoldShrinkEmpty));
         }
         for (int i = 0; i < 2; ++i) {
             sm100::mbar_init(sm100::smem_u32(&s_ready[i]), 1);
@@ -619,8 +620,11 @@ __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
     const int chunks = (C + 63) / 64;
     const int mine = (chunks - rank + nc - 1) / nc;  // this block's: rank, rank + nc, ...
     auto wait = [&](uint64_t* b, int phase) {
-        return sm100::mbar_wait_bounded(sm100::smem_u32(b), phase & 1, &s_abort, kTileWaitNs);
+        return sm100::mbar_wait_bounded(sm100::smem_u32(b), phase & 1, &s_abort, waits.ns);
     };
+    // For the roles that go on with collective instructions: a warp goes one way
+    // (lanes may see a late arrival and the abort flag in either order).
+    auto wait_warp = [&](uint64_t* b, int phase) { return __all_sync(0xFFFFFFFFu, wait(b, phase)) != 0; };
     constexpr int kPitch = RP + 4;
     float* const part = reinterpret_cast<float*>(ring);
     float sum[RP];
@@ -629,8 +633,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
         for (int r = 0; r < RP; ++r) sum[r] = 0.0f;
         const int chains = (mine + kTileChain - 1) / kTileChain;
         for (int c = 0; c < chains; ++c) {
-            if (!wait(&s_ready[c & 1], c >> 1)) break;
-            __syncwarp();
+            if (!wait_warp(&s_ready[c & 1], c >> 1)) break;
             sm100::tc_fence_after();
 #pragma unroll
             for (int c0 = 0; c0 < RP; c0 += 16) {
@@ -677,8 +680,8 @@ __global__ void __launch_bounds__(kTileThreads, tile_blocks(RP))
             const uint64_t db0 = sm100::sw128_kmajor_desc(ring_s + kTileTokens * 128);
             int st = 0, turn = 0, step = 0, c = 0;
             for (int i = 0; i < mine; ++i) {
-                if (step == 0 && c >= 2 && !wait(&s_read[c & 1], (c >> 1) - 1)) break;
-                if (!wait(&s_full[st], turn)) break;
+                if (step == 0 && c >= 2 && !wait_warp(&s_read[c & 1], (c >> 1) - 1)) break;
+                if (!wait_warp(&s_full[st], turn)) break;
                 sm100::fence_proxy_async_smem();
                 sm100::tc_fence_after();
                 const uint64_t da = da0 + st * (kStage / 16), db = db0 + st * (kStage / 16);
@@ -1616,7 +1619,8 @@ cudaError_t shrink_tile(const LoraRows& rows, const uint16_t* x, int64_t ldx, in
     cudaError_t err = allow_smem<lora_shrink_tile_kernel<RP>>(tile_smem(RP));
     if (err != cudaSuccess) return err;
     Launch l(units * nc, kTileThreads, tile_smem(RP), s, nc, false);
-    return cudaLaunchKernelEx(&l.cfg, lora_shrink_tile_kernel<RP>, map, rows, x, ldx, C, R, scales, v, t, u, ut);
+    return cudaLaunchKernelEx(&l.cfg, lora_shrink_tile_kernel<RP>, map, rows, x, ldx, C, R, scales, v, t, u, ut,
+                              waits());
 }
 
 template <int RP>

@@ -34,7 +34,7 @@ def test_gradient_without_tokens_waits_for_the_call_before(R):
 
 
 # barriers of moe_debug_waits
-EXPAND_SLAB, EXPAND_FREE = 1, 2
+EXPAND_SLAB, EXPAND_FREE, SHRINK_FULL, SHRINK_EMPTY = 1, 2, 4, 8
 LIMIT_NS = 50_000_000
 
 
@@ -78,4 +78,37 @@ def test_expand_whose_wait_runs_out(held, barrier, R):
     if barrier == EXPAND_SLAB:                             # no product without its rank rows
         assert bool(gone.all())
     for p, q in zip(forward(), (v, out, o16)):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("T,R", [(600, 16), (600, 64), (700, 100), (9000, 64)])
+@pytest.mark.parametrize("barrier", [SHRINK_FULL, SHRINK_EMPTY])
+def test_shrink_whose_wait_runs_out(held, barrier, T, R):
+    """Where a wait of the tiled shrink runs out, v and all that is made of it
+    are NaN; rows without an adapter stay, and the next call is right."""
+    K, N, n = 4096, 264, 3
+    g = torch.Generator(device="cuda").manual_seed(T + R)
+
+    def rnd(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    x, a, b = rnd(T, K), rnd(n, R, K), rnd(n, R, N)
+    ids = torch.arange(T, dtype=torch.int32, device="cuda") % (n + 1) - 1
+    batch = LoraBatch(n, T).assign(ids)
+    base, has = torch.randn((T, N), generator=g, device="cuda"), ids >= 0
+
+    def forward():
+        v, out = torch.full((T, R), -7.0, device="cuda"), base.clone()
+        fm.moe_lora(x, a, b, None, batch.offsets, batch.sorted, out, v, out)
+        return v, out
+
+    v, out = forward()
+    held(barrier)
+    v1, out1 = forward()
+    torch.cuda.synchronize()
+    fm.moe_debug_waits(0, 0)
+    P = int(has.sum())
+    assert torch.isnan(v1[:P]).all() and torch.equal(v1[P:], v[P:])
+    assert torch.isnan(out1[has]).all() and torch.equal(out1[~has], base[~has])
+    for p, q in zip(forward(), (v, out)):
         assert torch.equal(p, q)
