@@ -211,6 +211,8 @@ enum : uint32_t {
     kHoldExpandFree = 1u << 1,  // ... base row buffer free again
     kHoldShrinkFull = 1u << 2,  // adapters, tiled shrink: stage in
     kHoldShrinkEmpty = 1u << 3, // ... stage used
+    kHoldOuterFull = 1u << 4,   // adapters, gradient product: stage in
+    kHoldOuterEmpty = 1u << 5,  // ... stage used
 };
 struct Waits {
     uint64_t ns;

@@ -508,7 +508,6 @@ __global__ void __launch_bounds__(kSmallThreads, 2) lora_small_kernel(LoraRows r
 constexpr int kTileTokens = 128;
 constexpr int kTileThreads = 288;  // four warps of sums, four producers, the issuer
 constexpr int kTileChain = 4;      // stages per accumulation chain
-constexpr uint64_t kTileWaitNs = 2000000000ull;
 
 constexpr int tile_stages(int RP) { return RP <= 32 ? 5 : RP <= 64 ? 4 : 6; }
 constexpr int tile_blocks(int RP) { return RP <= 64 ? 2 : 1; }  // per SM
@@ -1288,7 +1287,7 @@ __device__ __forceinline__ OuterItem outer_item(const LoraRows& rows, const int1
 __global__ void __launch_bounds__(kOuterThreads, 2)
     lora_outer_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       LoraRows rows, int R, int rblocks, OuterSide pa, OuterSide pb, int ablocks, int blocks,
-                      bool behind_expand)
+                      bool behind_expand, Waits waits)
 {
     constexpr int S = kOuterStages;
     extern __shared__ uint8_t dyn[];
@@ -1307,8 +1306,9 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
     const uint32_t ring_s = sm100::smem_u32(ring);
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            sm100::mbar_init(sm100::smem_u32(&s_full[i]), 128 + 1);  // the copies of x, the terms of v
-            sm100::mbar_init(sm100::smem_u32(&s_empty[i]), 1);
+            // the copies of x, the terms of v
+            sm100::mbar_init(sm100::smem_u32(&s_full[i]), 128 + 1 + waits.extra(kHoldOuterFull));
+            sm100::mbar_init(sm100::smem_u32(&s_empty[i]), 1 + waits.extra(kHoldOuterEmpty));
         }
         for (int i = 0; i < 2; ++i) {
             sm100::mbar_init(sm100::smem_u32(&s_ready[i]), 1);
@@ -1342,7 +1342,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
     sm100::tc_fence_after();
     const uint32_t tmem = s_tmem;
     auto wait = [&](uint64_t* b, int phase) {
-        return sm100::mbar_wait_bounded(sm100::smem_u32(b), phase & 1, &s_abort, kTileWaitNs);
+        return sm100::mbar_wait_bounded(sm100::smem_u32(b), phase & 1, &s_abort, waits.ns);
     };
     // this block's item of a round (there in even rounds, back in odd ones)
     auto item_of = [&](int64_t round) {
@@ -1363,9 +1363,9 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
 #pragma unroll
                 for (int u = 0; u < 16; ++u) sum[j][u] = 0.0f;
             for (int i = 0; i < o.stages; i += kOuterChain, ++c) {
-                ok = ok && wait(&s_ready[c & 1], c >> 1);
+                // a warp goes one way (lanes may see a late arrival and the abort flag in either order)
+                ok = __all_sync(0xFFFFFFFFu, ok && wait(&s_ready[c & 1], c >> 1));
                 if (!ok) break;
-                __syncwarp();
                 sm100::tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < kOuterCols / 32; ++j) {
@@ -1482,7 +1482,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
             int step = 0;
             for (int i = 0; i < o.stages; ++i) {
                 if (step == 0 && c >= 2) ok = ok && wait(&s_read[c & 1], (c >> 1) - 1);
-                ok = ok && wait(&s_full[st], turn);
+                ok = __all_sync(0xFFFFFFFFu, ok && wait(&s_full[st], turn));
                 if (!ok) break;
                 sm100::fence_proxy_async_smem();
                 sm100::tc_fence_after();
@@ -1748,7 +1748,7 @@ cudaError_t launch_lora_outer(const LoraRows& rows, int R, const LoraOuter& a, c
     // programmatic launch start while it still writes.
     Launch l(grid, kOuterThreads, kOuterSmem, s, nc, rows.T > 0);
     return cudaLaunchKernelEx(&l.cfg, lora_outer_kernel, map[0], map[1], rows, R, rblocks, side[0], side[1], ab,
-                              ab + bb, behind_expand);
+                              ab + bb, behind_expand, waits());
 }
 
 }  // namespace fp8moe

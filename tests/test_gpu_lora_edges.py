@@ -34,7 +34,7 @@ def test_gradient_without_tokens_waits_for_the_call_before(R):
 
 
 # barriers of moe_debug_waits
-EXPAND_SLAB, EXPAND_FREE, SHRINK_FULL, SHRINK_EMPTY = 1, 2, 4, 8
+EXPAND_SLAB, EXPAND_FREE, SHRINK_FULL, SHRINK_EMPTY, OUTER_FULL, OUTER_EMPTY = 1, 2, 4, 8, 16, 32
 LIMIT_NS = 50_000_000
 
 
@@ -111,4 +111,40 @@ def test_shrink_whose_wait_runs_out(held, barrier, T, R):
     assert torch.isnan(v1[:P]).all() and torch.equal(v1[P:], v[P:])
     assert torch.isnan(out1[has]).all() and torch.equal(out1[~has], base[~has])
     for p, q in zip(forward(), (v, out)):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("T,K,R,n", [(9000, 512, 64, 3), (9000, 1024, 64, 40), (3000, 256, 100, 2), (16000, 256, 8, 4)])
+@pytest.mark.parametrize("barrier", [OUTER_FULL, OUTER_EMPTY])
+def test_gradient_product_whose_wait_runs_out(held, barrier, T, K, R, n):
+    """Where a wait of the gradient product runs out the entries concerned are
+    NaN; the others and dx are right, and so is the next call."""
+    g = torch.Generator(device="cuda").manual_seed(T + R)
+
+    def rnd(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    x, dout, a, b = rnd(T, K), rnd(T, K), rnd(n, R, K), rnd(n, R, K)
+    batch = LoraBatch(n, T).assign(torch.arange(T, dtype=torch.int32, device="cuda") % n)
+    v = torch.randn((T, R), generator=g, device="cuda")
+
+    def backward():
+        dx = torch.full((T, K), -7.0, device="cuda")
+        d_a, d_b = torch.full((n, R, K), -7.0, device="cuda"), torch.full((n, R, K), -7.0, device="cuda")
+        ws = torch.empty((fm.moe_lora_backward_workspace_bytes(T, R),), dtype=torch.uint8, device="cuda")
+        fm.moe_lora_backward(x, a, b, None, batch.offsets, batch.sorted, v, dout, None, dx, d_a, d_b, ws)
+        return dx, d_a, d_b
+
+    want = backward()
+    held(barrier)
+    got = backward()
+    torch.cuda.synchronize()
+    fm.moe_debug_waits(0, 0)
+    assert torch.equal(got[0], want[0])
+    for p, q in zip(got[1:], want[1:]):
+        gone = torch.isnan(p)
+        assert bool(gone.any()) and torch.equal(p[~gone], q[~gone])
+        if barrier == OUTER_FULL:                          # no stage ever comes in
+            assert bool(gone.all())
+    for p, q in zip(backward(), want):
         assert torch.equal(p, q)
