@@ -213,6 +213,7 @@ enum : uint32_t {
     kHoldShrinkEmpty = 1u << 3, // ... stage used
     kHoldOuterFull = 1u << 4,   // adapters, gradient product: stage in
     kHoldOuterEmpty = 1u << 5,  // ... stage used
+    kHoldLoss = 1u << 6,        // losses: rows in
 };
 struct Waits {
     uint64_t ns;

@@ -21,6 +21,8 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <climits>
+
 #include "internal.h"
 #include "sm100.cuh"
 
@@ -332,15 +334,23 @@ __global__ void __launch_bounds__(kLossWarps * 32)
     }
 }
 
-// Many rows: per-block sums part [gridDim.x][E], part_z, part_n ...
+// Many rows: per-block sums part [gridDim.x][E], part_z, part_n ...  A block
+// that lacks rows (a wait ran out) writes NaN and a count below any sum of the
+// others'.
+constexpr int kLostRows = INT_MIN;
+// Counted tokens of a loss that lacks rows: negative, also once other ranks'
+// counts are added to it.
+constexpr int kNoCount = -(1 << 30);
 template <int VPL, int LPR>
-__device__ __forceinline__ void write_part(const LossSums& own, const float* s_sum, int E, float* __restrict__ part,
-                                           double* __restrict__ part_z, int* __restrict__ part_n)
+__device__ __forceinline__ void write_part(const LossSums& own, const float* s_sum, bool lost, int E,
+                                           float* __restrict__ part, double* __restrict__ part_z,
+                                           int* __restrict__ part_n)
 {
-    for (int e = threadIdx.x; e < E; e += kLossWarps * 32) part[static_cast<int64_t>(blockIdx.x) * E + e] = s_sum[e];
+    for (int e = threadIdx.x; e < E; e += kLossWarps * 32)
+        part[static_cast<int64_t>(blockIdx.x) * E + e] = lost ? NAN : s_sum[e];
     if (threadIdx.x == 0) {
-        part_z[blockIdx.x] = own.z;
-        part_n[blockIdx.x] = own.n;
+        part_z[blockIdx.x] = lost ? NAN : own.z;
+        part_n[blockIdx.x] = lost ? kLostRows : own.n;
     }
 }
 
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(kLossWarps * 32)
     __shared__ float s_sum[VPL * LPR];
     allow_next();
     const LossSums own = loss_sums<VPL, LPR>(logits, T, E, blockIdx.x, gridDim.x, s_sum);
-    write_part<VPL, LPR>(own, s_sum, E, part, part_z, part_n);
+    write_part<VPL, LPR>(own, s_sum, false, E, part, part_z, part_n);
 }
 
 // The same by bulk copies, for rows of whole 16-byte pieces: every warp has a
@@ -362,7 +372,6 @@ __global__ void __launch_bounds__(kLossWarps * 32)
 // it: 131072 x 256 in 40 us against 35.)
 constexpr int kLossRing = 3;
 constexpr int kLossChunk = 4096;  // bytes
-constexpr uint64_t kLossWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
 {
@@ -380,7 +389,7 @@ constexpr int rows_at_once()  // rows that a lane works on side by side
 template <int VPL, int LPR>
 __global__ void __launch_bounds__(kLossWarps * 32)
     balance_bulk_kernel(const float* __restrict__ logits, int64_t T, int E, int rows, float* __restrict__ part,
-                        double* __restrict__ part_z, int* __restrict__ part_n)
+                        double* __restrict__ part_z, int* __restrict__ part_n, Waits waits)
 {
     constexpr int kGroups = 32 / LPR, kOnce = rows_at_once<VPL>();
     extern __shared__ __align__(128) uint8_t ring[];
@@ -390,7 +399,7 @@ __global__ void __launch_bounds__(kLossWarps * 32)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     allow_next();
     if (lane == 0) {
-        for (int i = 0; i < kLossRing; ++i) sm100::mbar_init(sm100::smem_u32(&s_bar[warp][i]), 1);
+        for (int i = 0; i < kLossRing; ++i) sm100::mbar_init(sm100::smem_u32(&s_bar[warp][i]), 1 + waits.extra(kHoldLoss));
         sm100::fence_barrier_init();
     }
     if (threadIdx.x == 0) s_abort = 0;
@@ -412,7 +421,7 @@ __global__ void __launch_bounds__(kLossWarps * 32)
     int slot = 0, turn = 0;
     bool ok = true;
     for (int64_t t = t0; t < T; t += step) {
-        ok = ok && sm100::mbar_wait_bounded(sm100::smem_u32(&s_bar[warp][slot]), turn & 1, &s_abort, kLossWaitNs);
+        ok = ok && sm100::mbar_wait_bounded(sm100::smem_u32(&s_bar[warp][slot]), turn & 1, &s_abort, waits.ns);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         const int have = static_cast<int>(min(static_cast<int64_t>(rows), T - t));
         const float* const chunk = reinterpret_cast<const float*>(mine + slot * kLossChunk);
@@ -443,10 +452,10 @@ __global__ void __launch_bounds__(kLossWarps * 32)
             ++turn;
         }
     }
-    if (!ok) sums.z = NAN;  // a wait that ran out
     const LossSums own = join_warps<VPL, LPR>(sums, E, s_sum);
-    write_part<VPL, LPR>(own, s_sum, E, part, part_z, part_n);
-    if (s_abort) sm100::settle();
+    const bool lost = s_abort != 0;  // (every warp is past its waits)
+    write_part<VPL, LPR>(own, s_sum, lost, E, part, part_z, part_n);
+    if (lost) sm100::settle();
 }
 
 // ... summed by one cluster of eight blocks, which share the experts; the
@@ -508,7 +517,7 @@ __global__ void __launch_bounds__(kFinalThreads)
         for (int b = 0; b < kFinalBlocks; ++b) sum += s_term[b];
         loss[0] = static_cast<float>(E * sum / (P > 0 ? P : 1));
         loss[1] = static_cast<float>(z * inv_n);
-        counts[E] = static_cast<int32_t>(nd);
+        counts[E] = nd < 0.0 ? kNoCount : static_cast<int32_t>(nd);
     }
 }
 
@@ -535,7 +544,7 @@ __device__ __forceinline__ float balance_slopes(const int32_t* __restrict__ coun
 #pragma unroll
     for (int off = LPR / 2; off > 0; off >>= 1) P += __shfl_xor_sync(0xFFFFFFFFu, P, off);
     const int n = __ldg(counts + E);
-    const double inv_n = 1.0 / (n > 0 ? n : 1);
+    const double inv_n = n < 0 ? NAN : 1.0 / (n > 0 ? n : 1);  // negative: not counted (kNoCount)
     const float f = static_cast<float>(__ldg(d_loss) * E * inv_n / (P > 0.0 ? P : 1.0));
 #pragma unroll
     for (int i = 0; i < VPL; ++i) g[i] *= f;
@@ -815,7 +824,7 @@ cudaError_t balance(const float* logits, int64_t T, int E, const int32_t* offset
         err = allow_smem<balance_bulk_kernel<VPL, LPR>>(kLossWarps * kLossRing * kLossChunk);
         if (err != cudaSuccess) return err;
         balance_bulk_kernel<VPL, LPR><<<nb, kLossWarps * 32, kLossWarps * kLossRing * kLossChunk, s>>>(
-            logits, T, E, rows < most ? static_cast<int>(rows) : most, part, pz, pn);
+            logits, T, E, rows < most ? static_cast<int>(rows) : most, part, pz, pn, waits());
         err = cudaGetLastError();
     } else {
         balance_partial_kernel<VPL, LPR><<<nb, kLossWarps * 32, 0, s>>>(logits, T, E, part, pz, pn);

@@ -488,7 +488,9 @@ MOE_API int moe_combine_rows(const float* y, int64_t y_nrows, const int32_t* row
  *   ws, ws_bytes    scratch of at least moe_balance_loss_workspace_bytes(T, E)
  *
  * The sums over rows have a fixed order (FP32 inside a block, FP64 across
- * blocks): the same bits on every call.  The call records no device status.
+ * blocks): the same bits on every call.  The call records no device status;
+ * a wait inside the kernel that expires leaves NaN in loss and prob_mean and
+ * -2^30 for N, of which moe_route_backward makes NaN.
  * A workspace serves one call in flight (give captured graphs that may replay
  * side by side one each).
  * Limits: T >= 0, 1 <= E <= 1024.

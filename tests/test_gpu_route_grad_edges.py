@@ -42,3 +42,40 @@ def test_blocks_that_start_apart_join_alike(T, E):
     for g in got:
         for p, q in zip(g[:3], want[:3]):
             assert torch.equal(p, q)
+
+
+# barriers of moe_debug_waits
+LOSS = 64
+LIMIT_NS = 50_000_000
+
+
+@pytest.fixture
+def held():
+    yield lambda mask: fm.moe_debug_waits(LIMIT_NS, mask)
+    torch.cuda.synchronize()
+    fm.moe_debug_waits(0, 0)
+
+
+@pytest.mark.parametrize("T,E", [(4096, 256), (70001, 8), (2500, 512)])
+def test_loss_whose_wait_runs_out(held, T, E):
+    """Losses of rows that did not come in say so, and so does the gradient
+    that is taken with their counts; the pairs per expert do not depend on
+    them.  The next call is right."""
+    z = torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    off = _offsets(T, E, 2)
+    want = _loss_buffers(T, E)
+    fm.moe_balance_loss(z, off, *want)
+    held(LOSS)
+    loss, counts, mean, ws = _loss_buffers(T, E)
+    fm.moe_balance_loss(z, off, loss, counts, mean, ws)
+    torch.cuda.synchronize()
+    fm.moe_debug_waits(0, 0)
+    assert torch.isnan(loss).all() and torch.isnan(mean).all()
+    assert torch.equal(counts[:E], want[1][:E]) and int(counts[E]) == -2 ** 30
+    counts[E] += T          # as summed with another rank's
+    d = torch.zeros_like(z)
+    fm.moe_route_backward(z, None, None, None, None, 1.0, counts, torch.ones((2,), device="cuda"), d)
+    assert torch.isnan(d).all()
+    fm.moe_balance_loss(z, off, loss, counts, mean, ws)
+    for p, q in zip((loss, counts, mean), want):
+        assert torch.equal(p, q)
