@@ -214,6 +214,8 @@ enum : uint32_t {
     kHoldOuterFull = 1u << 4,   // adapters, gradient product: stage in
     kHoldOuterEmpty = 1u << 5,  // ... stage used
     kHoldLoss = 1u << 6,        // losses: rows in
+    kHoldGradFull = 1u << 7,    // routing gradient: stage in
+    kHoldGradEmpty = 1u << 8,   // ... stage used
 };
 struct Waits {
     uint64_t ns;

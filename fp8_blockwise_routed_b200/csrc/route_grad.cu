@@ -603,14 +603,14 @@ constexpr int kSlotBatch = 8;    // slots per stage
 constexpr int kMaxStages = 16;
 constexpr int kDotBufs = 8;      // tokens between dots and tails
 constexpr int kGradRing = 200 * 1024;
-constexpr uint64_t kGradWaitNs = 2000000000ull;
 
 template <int VPL>
 __global__ void __launch_bounds__(kGradThreads, 1)
     route_grad_kernel(const float* __restrict__ logits, int64_t T, int E, const int32_t* __restrict__ ids,
                       const float* __restrict__ w, int k, const float* __restrict__ y,
                       const uint16_t* __restrict__ dout, int H, float rs, const int32_t* __restrict__ counts,
-                      const float* __restrict__ d_loss, float* __restrict__ d_logits, int stages, int stage_bytes)
+                      const float* __restrict__ d_loss, float* __restrict__ d_logits, int stages, int stage_bytes,
+                      Waits waits)
 {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_dots[kDotBufs], s_done[kDotBufs];
@@ -619,8 +619,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
-            sm100::mbar_init(sm100::smem_u32(&s_full[i]), 1);
-            sm100::mbar_init(sm100::smem_u32(&s_empty[i]), kDotWarps);
+            sm100::mbar_init(sm100::smem_u32(&s_full[i]), 1 + waits.extra(kHoldGradFull));
+            sm100::mbar_init(sm100::smem_u32(&s_empty[i]), kDotWarps + waits.extra(kHoldGradEmpty));
         }
         for (int i = 0; i < kDotBufs; ++i) {
             sm100::mbar_init(sm100::smem_u32(&s_dots[i]), kDotWarps);
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     __syncthreads();
     auto wait = [&](uint64_t* b, int phase) {
-        return sm100::mbar_wait_bounded(sm100::smem_u32(b), phase & 1, &s_abort, kGradWaitNs);
+        return sm100::mbar_wait_bounded(sm100::smem_u32(b), phase & 1, &s_abort, waits.ns);
     };
     // slots of a token that hold an expert, as a mask
     auto load_id = [&](int64_t t) { return (t < T && lane < k) ? __ldg(ids + t * k + lane) : -1; };
@@ -651,8 +651,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
                 for (int u = 0; u < kSlotBatch; ++u) acc[u] = 0.0f;
                 for (int c0 = 0; c0 < H; c0 += kChunk) {
-                    ok = ok && wait(&s_full[st], turn);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                    ok = __all_sync(0xFFFFFFFFu, ok && wait(&s_full[st], turn));
+                    if (!ok) break;
                     const uint8_t* s = ring + st * stage_bytes;
                     const int c = threadIdx.x * 4;
                     if (c0 + c < H) {
@@ -688,7 +688,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 }
                 acc[0] += __shfl_xor_sync(0xFFFFFFFFu, acc[0], 2);
                 acc[0] += __shfl_xor_sync(0xFFFFFFFFu, acc[0], 1);
-                if ((lane & 3) == 0) s_red[buf][warp][j0 + lane / 4] = acc[0];
+                // NaN once a wait ran out: columns, or the tail's leave to write, are missing
+                if ((lane & 3) == 0) s_red[buf][warp][j0 + lane / 4] = ok ? acc[0] : NAN;
             }
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(sm100::smem_u32(&s_dots[buf]));
@@ -744,6 +745,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             const float wj = id >= 0 ? __ldg(w + t * k + lane) : 0.0f;
             const int buf = static_cast<int>(n % kDotBufs);
             ok = ok && wait(&s_dots[buf], static_cast<int>(n / kDotBufs));
+            // a dot warp that gave up arrives all the same, behind the flag
+            ok = __all_sync(0xFFFFFFFFu, ok && !*static_cast<volatile int*>(&s_abort));
             float s = 0.0f;
             if (id >= 0) {
 #pragma unroll
@@ -862,7 +865,7 @@ cudaError_t route_grad(const RouteGradArgs& a, int sm_count, cudaStream_t s)
     const unsigned grid = static_cast<unsigned>(a.T < sm_count ? a.T : sm_count);
     route_grad_kernel<VPL><<<grid, kGradThreads, stages * stage_bytes, s>>>(
         a.logits, a.T, a.E, a.ids, a.w, a.k, a.y, a.dout, a.H, a.rs, a.counts, a.d_loss, a.d_logits, stages,
-        stage_bytes);
+        stage_bytes, waits());
     return cudaGetLastError();
 }
 

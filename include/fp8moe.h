@@ -526,7 +526,8 @@ MOE_API int moe_balance_loss(const float* logits, int64_t T, int E, const int32_
  *   d_logits          [T, E]  FP32, written; must not overlap logits
  *
  * Limits: as moe_combine and moe_balance_loss.  The call needs no workspace
- * and records no device status.
+ * and records no device status; a wait inside the kernel that expires leaves
+ * NaN at the chosen experts of the tokens concerned.
  * ------------------------------------------------------------------------- */
 MOE_API int moe_route_backward(const float* logits, int64_t T, int E, const int32_t* topk_ids, const float* topk_w,
                                int top_k, const float* y, const uint16_t* dout, int H, float routed_scaling,

@@ -45,7 +45,7 @@ def test_blocks_that_start_apart_join_alike(T, E):
 
 
 # barriers of moe_debug_waits
-LOSS = 64
+LOSS, GRAD_FULL, GRAD_EMPTY = 64, 128, 256
 LIMIT_NS = 50_000_000
 
 
@@ -79,3 +79,40 @@ def test_loss_whose_wait_runs_out(held, T, E):
     fm.moe_balance_loss(z, off, loss, counts, mean, ws)
     for p, q in zip((loss, counts, mean), want):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("T,E,k,H", [(600, 64, 8, 5120), (450, 300, 10, 2048), (1000, 16, 2, 4096)])
+@pytest.mark.parametrize("barrier", [GRAD_FULL, GRAD_EMPTY])
+def test_routing_gradient_whose_wait_runs_out(held, barrier, T, E, k, H):
+    """A token whose slot rows did not come in has NaN at its chosen experts;
+    everything else of the gradient is right, and so is the next call."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    z = torch.randn((T, E), generator=g, device="cuda")
+    w, ids = torch.softmax(z, 1).topk(k, 1)
+    ids = ids.to(torch.int32)
+    ids[::5] = -1                                          # tokens without experts
+    y = torch.randn((T, k, H), generator=g, device="cuda")
+    dout = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    off, (loss, counts, mean, ws) = _offsets(T, E, k), _loss_buffers(T, E)
+    fm.moe_balance_loss(z, off, loss, counts, mean, ws)
+    d_loss = torch.ones((2,), device="cuda")
+
+    def backward():
+        d = torch.full((T, E), -7.0, device="cuda")
+        fm.moe_route_backward(z, ids, w, y, dout, 1.5, counts, d_loss, d)
+        return d
+
+    want = backward()
+    assert torch.isfinite(want).all()
+    held(barrier)
+    got = backward()
+    torch.cuda.synchronize()
+    fm.moe_debug_waits(0, 0)
+    chosen = torch.zeros((T, E), dtype=torch.bool, device="cuda")
+    t, j = torch.nonzero(ids >= 0, as_tuple=True)
+    chosen[t, ids[t, j].long()] = True
+    gone = torch.isnan(got)
+    assert bool(gone.any()) and not bool((gone & ~chosen).any()) and torch.equal(got[~gone], want[~gone])
+    if barrier == GRAD_FULL:
+        assert torch.equal(gone, chosen)
+    assert torch.equal(backward(), want)
