@@ -115,10 +115,14 @@ __device__ __forceinline__ void add2(float& x, float& y, float a0, float a1)
 // multiplied by; returns whether there is any, and log(sum exp) in lse.
 // 2^(v L - mL), L = log2 e, mL = m L rounded: the rounding of mL is the same
 // for the whole row, so it cancels in the probabilities, and its effect on
-// the sum is known exactly (delta) and taken out of the logarithm.  The sum
-// lies in [1, E], where lg2.approx is within 2^-22 and one Newton step makes
-// rcp.approx good to an ulp.  A +Inf logit gives NaN (Inf - Inf), as in the
-// router's weights.
+// the sum is known exactly (delta) and taken out of the logarithm.  That holds
+// while the rounding is small: below kOffsetMax it is at most 2^-11, so the
+// sum lies in [0.999, 1.001 E], where lg2.approx is within 2^-22 (relative to
+// values beyond 1) and one Newton step makes rcp.approx good to an ulp.  From
+// there on (half a step of mL reaches 126, FP32's whole range of exponents, at
+// |m| = 1.5e9) the maximum is subtracted first, one instruction more per
+// logit.  A +Inf logit gives NaN (Inf - Inf), as in the router's weights.
+constexpr float kOffsetMax = 16384.0f;
 template <int VPL, int LPR>
 __device__ __forceinline__ bool softmax_row(float (&v)[VPL], float& inv, float& lse)
 {
@@ -133,7 +137,7 @@ __device__ __forceinline__ bool softmax_row(float (&v)[VPL], float& inv, float& 
     const bool any = m != -INFINITY;
     const float mL = m * kL;
     float s0 = 0.0f, s1 = 0.0f, delta = 0.0f;
-    if (fabsf(mL) < INFINITY) {
+    if (fabsf(mL) < kOffsetMax) {
         delta = fmaf(m, kL, -mL);
 #pragma unroll
         for (int i = 0; i < VPL; i += 2) {
@@ -142,7 +146,7 @@ __device__ __forceinline__ bool softmax_row(float (&v)[VPL], float& inv, float& 
             v[i + 1] = sm100::ex2_approx_ftz(v[i + 1]);
             add2(s0, s1, v[i], v[i + 1]);
         }
-    } else {  // a maximum beyond FP32's range divided by L, an infinite one, or none
+    } else {  // a maximum far out, an infinite one, or none
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             v[i] = any ? sm100::ex2_approx_ftz((v[i] - m) * kL) : 0.0f;

@@ -1,9 +1,11 @@
 """moe_balance_loss and moe_route_backward at the edges of their ranges and
 beside other work."""
+import numpy as np
 import pytest
 import torch
 
 import fp8_blockwise_routed_b200 as fm
+from test_gpu_route_grad import U, _exact_grad, _exact_probs, _gamma, _grad_case, _loss, _route
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +118,66 @@ def test_routing_gradient_whose_wait_runs_out(held, barrier, T, E, k, H):
     if barrier == GRAD_FULL:
         assert torch.equal(gone, chosen)
     assert torch.equal(backward(), want)
+
+
+# Logits far out: whole rows of one value (a padded token masked with it), one
+# such logit beside ordinary ones, and it beside its negative.  The bounds are
+# those of the ordinary ranges (imported): an exponential is off by its
+# argument's rounding (u |z - max|, exact for logits within a factor two) and
+# by 4 u, so a row's probabilities do not lose by where its maximum lies; what
+# lies 104 or more below it is 0 in both.
+FAR = [1e9, 3e9, -1e9, 1e10, -1e10, -65504.0, 1e20, -1e20, 1e30, -1e30, 2e38, -2e38, 3.3e38]
+FAR_SHAPES = [(65, 8), (40, 24), (50, 48), (33, 130), (70, 256), (41, 300), (21, 1024), (4096, 256), (40001, 8),
+              (3001, 257)]
+
+
+def _far(z, val):
+    T, E = z.shape
+    z[::4] = val
+    z[1::8, E // 3] = val
+    z[5::8] = -val
+    z[5::8, E // 2] = val
+    return z
+
+
+@pytest.mark.parametrize("val", FAR)
+@pytest.mark.parametrize("T,E", FAR_SHAPES)
+def test_losses_of_far_logits(T, E, val):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    z = _far(torch.randn((T, E), generator=g, device="cuda") * 3, val)
+    ids, w, off = _route(z, 2)
+    assert torch.isfinite(w).all()                         # the router takes them
+    loss, counts, mean = _loss(z, off, fill=255)
+    p, lse, some, ep = _exact_probs(z)
+    c = counts[:-1].double().cpu().numpy()
+    assert int(counts[-1]) == T
+    want = p.mean(0)
+    tol = ep.mean(0) + (_gamma(T / 16 + 17) + U) * want
+    assert np.all(np.abs(mean.double().cpu().numpy() - want) <= tol)
+    wl = E * (c * want).sum() / c.sum()
+    assert abs(float(loss[0]) - wl) <= E * (c * tol).sum() / c.sum() + 2 * U * wl
+    wz = (lse ** 2).mean()
+    if wz < 1e38 and np.abs(lse).max() < 1e18:             # (beyond FP32's range: below)
+        el = U * (np.abs(lse) + 5 * np.log(max(E, 2)) + E / 32 + 32)
+        assert abs(float(loss[1]) - wz) <= (2 * np.abs(lse) * el + el ** 2).mean() + 18 * U * wz
+    elif wz > 4e38:
+        assert float(loss[1]) == np.inf
+
+
+@pytest.mark.parametrize("val", FAR)
+@pytest.mark.parametrize("T,E,k,H", [(45, 8, 2, 128), (33, 130, 3, 256), (40, 256, 8, 128), (29, 300, 4, 128),
+                                     (17, 1024, 9, 128)])
+def test_gradient_of_far_logits(T, E, k, H, val):
+    z, ids, w, off, y, dout = _grad_case(T, E, k, H, "plain", 2.5, seed=T)
+    _far(z, val)
+    ids, w, off = _route(z, k)
+    _, counts, _ = _loss(z, off)
+    d_loss = torch.tensor([0.7, -0.3], device="cuda")
+    for use_y, use_loss in ((True, True), (True, False), (False, True)):
+        d = torch.full((T, E), -7.0, device="cuda")
+        fm.moe_route_backward(z, ids if use_y else None, w if use_y else None, y if use_y else None,
+                              dout if use_y else None, 2.5, counts if use_loss else None,
+                              d_loss if use_loss else None, d)
+        want, tol = _exact_grad(z, ids, w, y if use_y else None, dout, 2.5, counts, d_loss if use_loss else None)
+        got = d.double().cpu().numpy()
+        assert np.all(np.abs(got - want) <= tol), (use_y, use_loss)
