@@ -555,22 +555,27 @@ __device__ __forceinline__ float balance_slopes(const int32_t* __restrict__ coun
     return static_cast<float>(2.0 * __ldg(d_loss + 1) * inv_n);
 }
 
-// A row's gradient from its logits v: balance and z terms, plus slot_d of lane
-// j at expert slot_id of lane j for the k slots.
+// A row's gradient from its logits v: balance and z terms (if losses), plus
+// slot_d of lane j at expert slot_id of lane j for the k slots.
 template <int VPL, int LPR>
-__device__ __forceinline__ void grad_row(float (&v)[VPL], const float (&g)[VPL], float zc, int E, int k, int slot_id,
-                                         float slot_d, float* __restrict__ dst, int lane, bool ok)
+__device__ __forceinline__ void grad_row(float (&v)[VPL], bool losses, const float (&g)[VPL], float zc, int E, int k,
+                                         int slot_id, float slot_d, float* __restrict__ dst, int lane, bool ok)
 {
-    float inv, lse, inner = 0.0f;
-    softmax_row<VPL, LPR>(v, inv, lse);
+    if (losses) {
+        float inv, lse, inner = 0.0f;
+        softmax_row<VPL, LPR>(v, inv, lse);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        v[i] *= inv;
-        inner += v[i] * g[i];
+        for (int i = 0; i < VPL; ++i) {
+            v[i] *= inv;
+            inner += v[i] * g[i];
+        }
+        inner = row_sum<LPR>(inner) - zc * lse;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] *= g[i] - inner;
+    } else {  // 0 times the softmax would pass on the NaN of a +Inf logit
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] = 0.0f;
     }
-    inner = row_sum<LPR>(inner) - zc * lse;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] *= g[i] - inner;
     for (int j = 0; j < k; ++j) {
         const int id = __shfl_sync(0xFFFFFFFFu, slot_id, j);
         const float d = __shfl_sync(0xFFFFFFFFu, slot_d, j);
@@ -761,7 +766,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(sm100::smem_u32(&s_done[buf]));
             const float total = row_sum<32>(s);
-            grad_row<VPL, 32>(v, g, zc, E, k, id, s - wj * total, d_logits + t * E, lane, true);
+            grad_row<VPL, 32>(v, d_loss != nullptr, g, zc, E, k, id, s - wj * total, d_logits + t * E, lane, true);
         }
     }
     __syncthreads();
@@ -785,7 +790,7 @@ __global__ void __launch_bounds__(kBalanceGradThreads)
         const int64_t t = t0 + lane / LPR;
         float v[VPL];
         load_row<VPL, LPR>(logits + t * E, E, lane, t < T, v);
-        grad_row<VPL, LPR>(v, g, zc, E, 0, -1, 0.0f, d_logits + t * E, lane, t < T);
+        grad_row<VPL, LPR>(v, true, g, zc, E, 0, -1, 0.0f, d_logits + t * E, lane, t < T);
     }
 }
 

@@ -181,3 +181,22 @@ def test_gradient_of_far_logits(T, E, k, H, val):
         want, tol = _exact_grad(z, ids, w, y if use_y else None, dout, 2.5, counts, d_loss if use_loss else None)
         got = d.double().cpu().numpy()
         assert np.all(np.abs(got - want) <= tol), (use_y, use_loss)
+
+
+def test_without_losses_no_softmax_takes_part():
+    """d_loss None leaves the routing weights' part alone: a +Inf logit, whose
+    softmax is NaN, reaches the chosen experts of its own row only (through
+    the router's NaN weights)."""
+    T, E, k, H = 23, 40, 3, 256
+    z, ids, w, off, y, dout = _grad_case(T, E, k, H, "plain", 2.5, seed=5)
+    z[3, 7] = torch.inf
+    ids, w, off = _route(z, k)
+    assert torch.isnan(w[3]).all()
+    d = torch.full((T, E), -7.0, device="cuda")
+    fm.moe_route_backward(z, ids, w, y, dout, 2.5, None, None, d)
+    keep = torch.arange(T, device="cuda") != 3
+    want, tol = _exact_grad(z[keep], ids[keep], w[keep], y[keep], dout[keep], 2.5, None, None)
+    assert np.all(np.abs(d[keep].double().cpu().numpy() - want) <= tol)
+    others = torch.ones((E,), dtype=torch.bool, device="cuda")
+    others[ids[3].long()] = False
+    assert torch.isnan(d[3][~others]).all() and not d[3][others].any()
