@@ -182,7 +182,10 @@ struct WarpSums {
     {
         float inv, lse;
         if (softmax_row<VPL, LPR>(v, inv, lse)) {
-            zf = fmaf(lse, lse, zf);
+            if (fabsf(lse) < 0x1p60f)  // 16 squares stay within FP32
+                zf = fmaf(lse, lse, zf);
+            else
+                z += static_cast<double>(lse) * lse;
             if ((++n & 15) == 0) {
                 z += zf;
                 zf = 0.0f;

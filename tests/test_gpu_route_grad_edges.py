@@ -200,3 +200,16 @@ def test_without_losses_no_softmax_takes_part():
     others = torch.ones((E,), dtype=torch.bool, device="cuda")
     others[ids[3].long()] = False
     assert torch.isnan(d[3][~others]).all() and not d[3][others].any()
+
+
+@pytest.mark.parametrize("T,E", [(4096, 256), (1000, 16), (3001, 257), (40001, 8)])
+def test_z_loss_of_a_few_far_rows(T, E):
+    """Squares beyond FP32's range do not lose a mean within it.  lse is off by
+    u (|lse| + ...) as above: relative 2 u + u from far rows, and the sum of 16
+    ordinary ones in FP32 does not matter beside them."""
+    z = torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(9), device="cuda")
+    z[5], z[T - 2] = -1e20, 3e19
+    ids, w, off = _route(z, 2)
+    loss, counts, _ = _loss(z, off)
+    want = ((z[5, 0].double() ** 2 + z[T - 2, 0].double() ** 2) / T).item()
+    assert 1e34 < want < 1e38 and abs(float(loss[1]) - want) <= 8 * U * want
