@@ -572,9 +572,16 @@ __device__ __forceinline__ void grad_row(float (&v)[VPL], bool losses, const flo
             v[i] *= inv;
             inner += v[i] * g[i];
         }
-        inner = row_sum<LPR>(inner) - zc * lse;
+        inner = row_sum<LPR>(inner);
+        const float slope = zc * lse;
+        if (fabsf(slope) < INFINITY) {
+            inner -= slope;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) v[i] *= g[i] - inner;
+            for (int i = 0; i < VPL; ++i) v[i] *= g[i] - inner;
+        } else {  // times the probability first: in range where the product is, 0 where p is
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) v[i] = fmaf(v[i] * zc, lse, v[i] * (g[i] - inner));
+        }
     } else {  // 0 times the softmax would pass on the NaN of a +Inf logit
 #pragma unroll
         for (int i = 0; i < VPL; ++i) v[i] = 0.0f;

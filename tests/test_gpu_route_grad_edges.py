@@ -213,3 +213,25 @@ def test_z_loss_of_a_few_far_rows(T, E):
     loss, counts, _ = _loss(z, off)
     want = ((z[5, 0].double() ** 2 + z[T - 2, 0].double() ** 2) / T).item()
     assert 1e34 < want < 1e38 and abs(float(loss[1]) - want) <= 8 * U * want
+
+
+def test_gradient_where_the_z_slope_is_beyond_fp32():
+    """2 d1 lse / N beyond FP32's range: its products with the probabilities
+    are finite where they lie within it, and 0 at logits that are not
+    selectable.  Relative bound: p as above (E / 32 + 32 units) and three
+    products; the balance term, 1e-6 of it at most, is included in `want`."""
+    T, E = 6, 1024
+    z = torch.full((T, E), -3e38, device="cuda")
+    z[:, ::2] = -torch.inf
+    z[4:] = torch.randn((2, E), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    counts = torch.full((E + 1,), 12, dtype=torch.int32, device="cuda")
+    counts[E] = T
+    d_loss = torch.tensor([0.5, 700.0], device="cuda")
+    d = torch.full((T, E), -7.0, device="cuda")
+    fm.moe_route_backward(z, None, None, None, None, 1.0, counts, d_loss, d)
+    want, tol = _exact_grad(z, None, None, None, None, 1.0, counts, d_loss)
+    slope = 2 * 700.0 / T * 3e38
+    assert slope > 3.5e38 and np.abs(want).max() < 3e38
+    assert not d[:4, ::2].any()
+    got = d.double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= np.maximum(tol, (E / 32 + 48) * U * np.abs(want)))
