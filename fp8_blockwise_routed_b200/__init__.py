@@ -238,6 +238,23 @@ def _call(fn, what: str, dev: int, stream, *args):
         _check(code, what)
 
 
+def _empty(shape, dtype, dev, stream):
+    """torch.empty for what a call on `stream` writes first (None: the current
+    one).  Allocated on that stream, so no work elsewhere still uses the
+    memory; known to the current stream, so it is not handed out again while
+    the caller's work there uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if here != stream:
+        t.record_stream(here)
+    return t
+
+
 # ------------------------------------------------------------------ sizes
 
 def moe_route_workspace_bytes(T: int, E: int, top_k: int) -> int:
@@ -688,11 +705,11 @@ class _RouterGradient:
         assert T <= self.max_tokens and logits.shape == (T, self.E)
         if getattr(self, "loss", None) is None:
             dev = self.offsets.device
-            self.loss = torch.empty((2,), dtype=torch.float32, device=dev)
-            self.counts = torch.empty((self.E + 1,), dtype=torch.int32, device=dev)
-            self.prob_mean = torch.empty((self.E,), dtype=torch.float32, device=dev)
-            self.ws_loss = torch.empty((moe_balance_loss_workspace_bytes(self.max_tokens, self.E),),
-                                       dtype=torch.uint8, device=dev)
+            self.counts = _empty((self.E + 1,), torch.int32, dev, stream)
+            self.prob_mean = _empty((self.E,), torch.float32, dev, stream)
+            self.ws_loss = _empty((moe_balance_loss_workspace_bytes(self.max_tokens, self.E),), torch.uint8, dev,
+                                  stream)
+            self.loss = _empty((2,), torch.float32, dev, stream)
         moe_balance_loss(logits, self.offsets, self.loss, self.counts, self.prob_mean, self.ws_loss, stream)
         return self.loss, self.counts
 
@@ -704,7 +721,7 @@ class _RouterGradient:
         assert T <= self.max_tokens and logits.shape == (T, self.E)
         assert d_loss is None or getattr(self, "counts", None) is not None, "balance_loss comes first"
         if d_logits is None:
-            d_logits = torch.empty((T, self.E), dtype=torch.float32, device=logits.device)
+            d_logits = _empty((T, self.E), torch.float32, logits.device, stream)
         moe_route_backward(logits, self.ids[:T], self.tw[:T], None if dout is None else self.y[:T], dout, self.rs,
                            None if d_loss is None else self.counts, d_loss, d_logits, stream)
         return d_logits

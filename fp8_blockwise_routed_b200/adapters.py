@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (moe_lora, moe_lora_backward, moe_lora_backward_workspace_bytes, moe_permute,
+from . import (_empty, moe_lora, moe_lora_backward, moe_lora_backward_workspace_bytes, moe_permute,
                moe_route_workspace_bytes)
 
 
@@ -72,10 +72,10 @@ class LoraAdapters:
         assert T == batch.T and T <= self.max_tokens and batch.n == self.n
         if self._grad is None:
             dev = self.a.device
-            self._grad = (torch.empty(self.a.shape, dtype=torch.float32, device=dev),
-                          torch.empty(self.b.shape, dtype=torch.float32, device=dev),
-                          torch.empty((moe_lora_backward_workspace_bytes(self.max_tokens, self.rank),),
-                                      dtype=torch.uint8, device=dev))
+            self._grad = (_empty(self.a.shape, torch.float32, dev, stream),
+                          _empty(self.b.shape, torch.float32, dev, stream),
+                          _empty((moe_lora_backward_workspace_bytes(self.max_tokens, self.rank),), torch.uint8, dev,
+                                 stream))
         d_a, d_b, ws = self._grad
         moe_lora_backward(x, self.a, self.b, self.scales, batch.offsets, batch.sorted, self.v[:T], dout, dx_base, dx,
                           d_a, d_b, ws, stream)
