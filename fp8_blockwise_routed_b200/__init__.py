@@ -694,15 +694,41 @@ def moe_lora_backward(x, lora_a, lora_b, scales, adapter_offsets, sorted_tokens,
 
 # ------------------------------------------------------------------ layer
 
+def _capturing(t) -> bool:
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
 class _RouterGradient:
     """The router's losses and gradient of a layer class, from the routing
-    and slot rows that its last forward call left in its buffers."""
+    and slot rows that its last forward call left in its buffers.  Both are
+    refused for a batch of another size than that call's, and the losses'
+    gradient when balance_loss has not been called since it; once one of
+    these calls is captured into a graph, whose replays are not seen here,
+    that is the caller's to keep."""
+
+    _routed = None      # tokens of the last forward call
+    _counted = False    # balance_loss called since
+    _captured = False
+
+    def _forwarded(self, x):
+        self._routed, self._counted = x.shape[0], False
+        if _capturing(x):
+            self._captured = True
+
+    def _of_last_forward(self, what: str, logits):
+        T = logits.shape[0]
+        assert T <= self.max_tokens and logits.shape == (T, self.E)
+        if self._routed is None:
+            _refuse(what, "forward comes first")
+        if T != self._routed and not self._captured:
+            _refuse(what, f"the last forward call was of {self._routed} tokens, not {T}")
+        return T
 
     def balance_loss(self, logits: torch.Tensor, stream=None):
         """(loss [2], counts [E+1]) of the batch that forward routed last:
-        balance and z loss, pairs per expert and counted tokens."""
-        T = logits.shape[0]
-        assert T <= self.max_tokens and logits.shape == (T, self.E)
+        balance and z loss, pairs per expert and counted tokens.  The buffers
+        are the layer's; the next call overwrites them."""
+        self._of_last_forward("balance_loss", logits)
         if getattr(self, "loss", None) is None:
             dev = self.offsets.device
             self.counts = _empty((self.E + 1,), torch.int32, dev, stream)
@@ -711,15 +737,19 @@ class _RouterGradient:
                                   stream)
             self.loss = _empty((2,), torch.float32, dev, stream)
         moe_balance_loss(logits, self.offsets, self.loss, self.counts, self.prob_mean, self.ws_loss, stream)
+        self._counted = True
+        if _capturing(logits):
+            self._captured = True
         return self.loss, self.counts
 
     def router_backward(self, logits: torch.Tensor, dout, d_loss=None, d_logits=None, stream=None) -> torch.Tensor:
         """d_logits [T, E] for dout [T, H] BF16 (the gradient of forward's
         rows; None: not through the routing weights) and d_loss [2] FP32 (of
         balance_loss's terms; None: without them)."""
-        T = logits.shape[0]
-        assert T <= self.max_tokens and logits.shape == (T, self.E)
-        assert d_loss is None or getattr(self, "counts", None) is not None, "balance_loss comes first"
+        what = "router_backward"
+        T = self._of_last_forward(what, logits)
+        if d_loss is not None and not self._counted and (not self._captured or getattr(self, "counts", None) is None):
+            _refuse(what, "balance_loss comes first (the counts are not those of the last forward call)")
         if d_logits is None:
             d_logits = _empty((T, self.E), torch.float32, logits.device, stream)
         moe_route_backward(logits, self.ids[:T], self.tw[:T], None if dout is None else self.y[:T], dout, self.rs,
@@ -765,6 +795,7 @@ class RoutedMoE(_RouterGradient):
         tokens, whose rows are added to the layer's."""
         T = x.shape[0]
         assert T <= self.max_tokens and x.shape[1] == self.H and logits.shape == (T, self.E)
+        self._forwarded(x)
         codes, scales = self.codes[:T], self.scales[:T]
         ids, tw, srt = self.ids[:T], self.tw[:T], self.sorted[: T * self.k]
         y, out = self.y[:T], self.out[:T]
@@ -832,6 +863,7 @@ class RoutedMoEMX(_RouterGradient):
         adapters, batch: as RoutedMoE.forward."""
         T = x.shape[0]
         assert T <= self.max_tokens and x.shape[1] == self.H and logits.shape == (T, self.E)
+        self._forwarded(x)
         codes, scales = self.codes[:T], self.scales[:T]
         ids, tw, srt = self.ids[:T], self.tw[:T], self.sorted[: max(T * self.k, 1)]
         y, out = self.y[:T], self.out[:T]

@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (_empty, moe_lora, moe_lora_backward, moe_lora_backward_workspace_bytes, moe_permute,
+from . import (_capturing, _empty, _refuse, moe_lora, moe_lora_backward, moe_lora_backward_workspace_bytes, moe_permute,
                moe_route_workspace_bytes)
 
 
@@ -47,15 +47,20 @@ class LoraAdapters:
     [n, rank, N] BF16 (rank-major: lora_b is the transpose of an output
     projection's [N, rank]), scales [n] FP32 or None, and the buffer of the
     shrunk rows for up to ``max_tokens`` tokens.  A backward call uses the
-    rows of the forward call before it."""
+    rows of the forward call before it (zeros if there was none), and is
+    refused for a batch of another size than that call's; once forward is
+    captured into a graph, whose replays are not seen here, that is the
+    caller's to keep."""
 
     def __init__(self, lora_a, lora_b, scales, max_tokens: int):
         self.a, self.b, self.scales = lora_a, lora_b, scales
         self.n, self.rank, self.K = lora_a.shape
         self.N = lora_b.shape[2]
         self.max_tokens = int(max_tokens)
-        self.v = torch.empty((self.max_tokens, self.rank), dtype=torch.float32, device=lora_a.device)
+        self.v = torch.zeros((self.max_tokens, self.rank), dtype=torch.float32, device=lora_a.device)
         self._grad = None
+        self._last = None       # tokens of the last forward call
+        self._captured = False
 
     def forward(self, batch: LoraBatch, x, base, out, out_bf16=None, stream=None):
         """out = base + the adapters' rows, for the tokens that have one;
@@ -63,6 +68,9 @@ class LoraAdapters:
         T = x.shape[0]
         assert T == batch.T and T <= self.max_tokens and batch.n == self.n
         moe_lora(x, self.a, self.b, self.scales, batch.offsets, batch.sorted, base, self.v[:T], out, out_bf16, stream)
+        self._last = T
+        if _capturing(x):
+            self._captured = True
         return out
 
     def backward(self, batch: LoraBatch, x, dout, dx_base=None, dx=None, stream=None):
@@ -70,6 +78,8 @@ class LoraAdapters:
         dx_base plus the adapters' part for the tokens that have one."""
         T = x.shape[0]
         assert T == batch.T and T <= self.max_tokens and batch.n == self.n
+        if self._last not in (None, T) and not self._captured:
+            _refuse("LoraAdapters.backward", f"the last forward call was of {self._last} tokens, not {T}")
         if self._grad is None:
             dev = self.a.device
             self._grad = (_empty(self.a.shape, torch.float32, dev, stream),

@@ -1,0 +1,76 @@
+"""What the layer's and the adapters' gradient calls refuse, without a GPU: the
+kernels' calls are replaced by records of their arguments."""
+import pytest
+import torch
+
+import fp8_blockwise_routed_b200 as fm
+from fp8_blockwise_routed_b200 import adapters
+
+T, E, H, I, K = 6, 8, 256, 128, 2
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    seen = []
+    for name in ("moe_route_quant", "moe_quant_act_mx", "moe_route", "moe_grouped_ffn", "moe_grouped_ffn_mx",
+                 "moe_combine", "moe_balance_loss", "moe_route_backward"):
+        monkeypatch.setattr(fm, name, lambda *a, _n=name, **k: seen.append((_n, a)))
+    for name in ("moe_permute", "moe_lora", "moe_lora_backward"):
+        monkeypatch.setattr(adapters, name, lambda *a, _n=name, **k: seen.append((_n, a)))
+    monkeypatch.setattr(fm, "moe_mx_pack_scales", lambda s: s)
+    return seen
+
+
+def _layer(cls):
+    u8 = torch.uint8
+    w = [torch.zeros(s, dtype=u8) for s in ((E, I, H), (E, I, H), (E, H, I))]
+    s = [torch.zeros((E, 1, 1))] * 3
+    return cls(w[0], s[0], w[1], s[1], w[2], s[2], K, 1.0, 16)
+
+
+def _refused(call, *args, **kw):
+    with pytest.raises(fm.MoeError) as e:
+        call(*args, **kw)
+    assert e.value.code == 1
+    return str(e.value)
+
+
+@pytest.mark.parametrize("cls", [fm.RoutedMoE, fm.RoutedMoEMX])
+def test_gradient_of_another_batch_than_the_counts(calls, cls):
+    layer = _layer(cls)
+    x, z, dl = torch.zeros((T, H), dtype=torch.bfloat16), torch.zeros((T, E)), torch.ones((2,))
+    dout = torch.zeros((T, H), dtype=torch.bfloat16)
+    assert "forward comes first" in _refused(layer.router_backward, z, dout)
+    assert "forward comes first" in _refused(layer.balance_loss, z)
+    layer.forward(x, z, stream=0)
+    layer.router_backward(z, dout)                         # through the weights alone: no counts needed
+    assert "balance_loss comes first" in _refused(layer.router_backward, z, dout, dl)
+    layer.balance_loss(z)
+    layer.router_backward(z, dout, dl)
+    layer.router_backward(z, None, dl)
+    layer.forward(x, z, stream=0)
+    assert "balance_loss comes first" in _refused(layer.router_backward, z, dout, dl)
+    layer.balance_loss(z)
+    layer.router_backward(z, dout, dl)
+    assert "was of 6 tokens, not 5" in _refused(layer.router_backward, z[:5], dout[:5])
+    assert "was of 6 tokens, not 5" in _refused(layer.balance_loss, z[:5])
+    n = len(calls)
+    layer._captured = True                                 # replays are not seen: nothing is refused
+    layer.router_backward(z[:5], dout[:5], dl)
+    assert len(calls) == n + 1
+
+
+def test_adapter_gradient_of_another_batch(calls):
+    a, b = torch.zeros((2, 4, 16), dtype=torch.bfloat16), torch.zeros((2, 4, 8), dtype=torch.bfloat16)
+    ad, batch = adapters.LoraAdapters(a, b, None, 16), adapters.LoraBatch(2, 16, device="cpu")
+    ids = torch.zeros((T,), dtype=torch.int32)
+    x, dout = torch.zeros((T, 16), dtype=torch.bfloat16), torch.zeros((T, 8), dtype=torch.bfloat16)
+    assert not ad.v.any()                                  # a gradient before any forward is of zero rows
+    ad.backward(batch.assign(ids), x, dout)
+    ad.forward(batch, x, None, torch.zeros((T, 8)))
+    ad.backward(batch, x, dout)
+    batch.assign(ids[:4])
+    assert "was of 6 tokens, not 4" in _refused(ad.backward, batch, x[:4], dout[:4])
+    ad.forward(batch, x[:4], None, torch.zeros((4, 8)))
+    ad.backward(batch, x[:4], dout[:4])
+    assert [c[0] for c in calls].count("moe_lora_backward") == 3

@@ -108,3 +108,20 @@ def test_first_adapter_gradient_on_another_stream():
     torch.cuda.synchronize()
     for p, q in zip(got, want):
         assert torch.equal(p, q)
+
+
+def test_gradient_after_a_replayed_forward():
+    """A replay is not seen by the layer: after it the gradient of the captured
+    batch is taken, whatever batch was routed eagerly in between."""
+    wl, d, layer = _layer(50)
+    dout = torch.randn((50, wl.H), device="cuda").to(torch.bfloat16)
+    d_loss = torch.tensor([0.01, 0.001], device="cuda")
+    layer.balance_loss(d["logits"])
+    want = layer.router_backward(d["logits"], dout, d_loss).clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.forward(d["x"], d["logits"])
+        layer.balance_loss(d["logits"])
+    layer.forward(d["x"][:30], d["logits"][:30])
+    graph.replay()
+    assert torch.equal(layer.router_backward(d["logits"], dout, d_loss), want)
