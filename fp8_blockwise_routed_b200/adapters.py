@@ -58,7 +58,7 @@ class LoraAdapters:
         self.N = lora_b.shape[2]
         self.max_tokens = int(max_tokens)
         self.v = torch.zeros((self.max_tokens, self.rank), dtype=torch.float32, device=lora_a.device)
-        self._grad = None
+        self._grad = self._ws = None
         self._last = None       # tokens of the last forward call
         self._captured = False
 
@@ -73,20 +73,24 @@ class LoraAdapters:
             self._captured = True
         return out
 
-    def backward(self, batch: LoraBatch, x, dout, dx_base=None, dx=None, stream=None):
+    def backward(self, batch: LoraBatch, x, dout, dx_base=None, dx=None, stream=None, d_a=None, d_b=None):
         """(d_a, d_b) FP32 for dout [T, N] BF16; dx, if given, receives
-        dx_base plus the adapters' part for the tokens that have one."""
+        dx_base plus the adapters' part for the tokens that have one.  d_a,
+        d_b: where to write the gradients; without them they go to buffers of
+        this object, which the next call overwrites (add them up before it)."""
         T = x.shape[0]
         assert T == batch.T and T <= self.max_tokens and batch.n == self.n
         if self._last not in (None, T) and not self._captured:
             _refuse("LoraAdapters.backward", f"the last forward call was of {self._last} tokens, not {T}")
-        if self._grad is None:
-            dev = self.a.device
+        dev = self.a.device
+        if self._ws is None:
+            self._ws = _empty((moe_lora_backward_workspace_bytes(self.max_tokens, self.rank),), torch.uint8, dev,
+                              stream)
+        if (d_a is None or d_b is None) and self._grad is None:
             self._grad = (_empty(self.a.shape, torch.float32, dev, stream),
-                          _empty(self.b.shape, torch.float32, dev, stream),
-                          _empty((moe_lora_backward_workspace_bytes(self.max_tokens, self.rank),), torch.uint8, dev,
-                                 stream))
-        d_a, d_b, ws = self._grad
+                          _empty(self.b.shape, torch.float32, dev, stream))
+        d_a = self._grad[0] if d_a is None else d_a
+        d_b = self._grad[1] if d_b is None else d_b
         moe_lora_backward(x, self.a, self.b, self.scales, batch.offsets, batch.sorted, self.v[:T], dout, dx_base, dx,
-                          d_a, d_b, ws, stream)
+                          d_a, d_b, self._ws, stream)
         return d_a, d_b

@@ -74,3 +74,22 @@ def test_adapter_gradient_of_another_batch(calls):
     ad.forward(batch, x[:4], None, torch.zeros((4, 8)))
     ad.backward(batch, x[:4], dout[:4])
     assert [c[0] for c in calls].count("moe_lora_backward") == 3
+
+
+def test_gradients_of_micro_batches_are_kept(calls):
+    """Buffers given by the caller take the gradients; the object's own are
+    made only where they are used, and are the same ones every time."""
+    a, b = torch.zeros((2, 4, 16), dtype=torch.bfloat16), torch.zeros((2, 4, 8), dtype=torch.bfloat16)
+    ad, batch = adapters.LoraAdapters(a, b, None, 16), adapters.LoraBatch(2, 16, device="cpu")
+    x, dout = torch.zeros((T, 16), dtype=torch.bfloat16), torch.zeros((T, 8), dtype=torch.bfloat16)
+    ad.forward(batch.assign(torch.zeros((T,), dtype=torch.int32)), x, None, torch.zeros((T, 8)))
+    mine = [(torch.zeros(a.shape), torch.zeros(b.shape)) for _ in range(2)]
+    for d_a, d_b in mine:
+        got = ad.backward(batch, x, dout, d_a=d_a, d_b=d_b)
+        assert got[0] is d_a and got[1] is d_b
+        assert calls[-1][0] == "moe_lora_backward" and calls[-1][1][10] is d_a and calls[-1][1][11] is d_b
+    assert ad._grad is None
+    one = ad.backward(batch, x, dout)
+    assert one[0].shape == a.shape and one[1].shape == b.shape and one[0].dtype == torch.float32
+    two = ad.backward(batch, x, dout, d_b=mine[0][1])
+    assert two[0] is one[0] and two[1] is mine[0][1]

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import fp8_blockwise_routed_b200 as fm
-from fp8_blockwise_routed_b200.adapters import LoraBatch
+from fp8_blockwise_routed_b200.adapters import LoraAdapters, LoraBatch
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +148,36 @@ def test_gradient_product_whose_wait_runs_out(held, barrier, T, K, R, n):
             assert bool(gone.all())
     for p, q in zip(backward(), want):
         assert torch.equal(p, q)
+
+
+def test_micro_batches_add_up():
+    """Gradients of two micro-batches in buffers of their own add up to those
+    of the whole batch (rounded apart: 2^-24 each, over at most 3 * 40 / 16 + 64
+    additions of either side, relative to the sums of absolute products)."""
+    K, N, R, n = 64, 48, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def rnd(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    x, dout, a, b = rnd(80, K), rnd(80, N), rnd(n, R, K), rnd(n, R, N)
+    ids = torch.arange(80, dtype=torch.int32, device="cuda") % n
+    ad = LoraAdapters(a, b, None, 80)
+    batch, out = LoraBatch(n, 80), torch.empty((80, N), device="cuda")
+    got = []
+    for lo in (0, 40):
+        batch.assign(ids[lo:lo + 40])
+        ad.forward(batch, x[lo:lo + 40], None, out[:40])
+        got.append(ad.backward(batch, x[lo:lo + 40], dout[lo:lo + 40], d_a=torch.empty(a.shape, device="cuda"),
+                               d_b=torch.empty(b.shape, device="cuda")))
+    batch.assign(ids)
+    ad.forward(batch, x, None, out)
+    whole = ad.backward(batch, x, dout)
+    u = 2.0 ** -24
+    for i in range(n):
+        t = ids == i
+        xa, da = x[t].double().abs(), dout[t].double().abs()
+        dv, v = da @ b[i].double().abs().T, xa @ a[i].double().abs().T
+        for w, p, q, mag in ((whole[0], got[0][0], got[1][0], dv.T @ xa), (whole[1], got[0][1], got[1][1], v.T @ da)):
+            diff = (w[i].double() - p[i].double() - q[i].double()).abs()
+            assert bool((diff <= 4 * (72 + 72) * 2 * u * mag).all())
