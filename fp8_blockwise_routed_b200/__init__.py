@@ -9,6 +9,7 @@ sm_100 GPU, calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -693,6 +694,13 @@ def moe_lora_backward(x, lora_a, lora_b, scales, adapter_offsets, sorted_tokens,
 
 
 # ------------------------------------------------------------------ layer
+
+def _device_of(t):
+    """Context with t's CUDA device current."""
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        return torch.cuda.device(t.get_device())
+    return contextlib.nullcontext()
+
 
 def _capturing(t) -> bool:
     return t.is_cuda and torch.cuda.is_current_stream_capturing()

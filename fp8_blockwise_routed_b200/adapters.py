@@ -13,8 +13,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (_capturing, _empty, _refuse, moe_lora, moe_lora_backward, moe_lora_backward_workspace_bytes, moe_permute,
-               moe_route_workspace_bytes)
+from . import (_capturing, _device_of, _empty, _refuse, moe_lora, moe_lora_backward,
+               moe_lora_backward_workspace_bytes, moe_permute, moe_route_workspace_bytes)
 
 
 class LoraBatch:
@@ -38,7 +38,8 @@ class LoraBatch:
         assert T <= self.max_tokens and adapter_ids.shape == (T,) and adapter_ids.dtype == torch.int32
         assert adapter_ids.is_contiguous() and adapter_ids.device == self.offsets.device
         self.T = T
-        moe_permute(adapter_ids.view(T, 1), self.n, self.offsets, self._sorted, self.ws, stream)
+        with _device_of(adapter_ids):
+            moe_permute(adapter_ids.view(T, 1), self.n, self.offsets, self._sorted, self.ws, stream)
         return self
 
 

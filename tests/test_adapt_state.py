@@ -93,3 +93,47 @@ def test_gradients_of_micro_batches_are_kept(calls):
     assert one[0].shape == a.shape and one[1].shape == b.shape and one[0].dtype == torch.float32
     two = ad.backward(batch, x, dout, d_b=mine[0][1])
     assert two[0] is one[0] and two[1] is mine[0][1]
+
+
+def test_batch_on_another_device_than_the_current_one(monkeypatch):
+    """assign groups on the device of the ids: its kernels are launched with
+    that device (and so its current stream) current."""
+    current = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    class Ids:                                             # a tensor on the second device
+        shape, dtype, device, is_cuda = (T,), torch.int32, "cuda:1", True
+
+        def is_contiguous(self):
+            return True
+
+        def get_device(self):
+            return 1
+
+        def view(self, *shape):
+            return self
+
+    seen = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(adapters, "moe_permute", lambda *a: seen.append(current[0]))
+    batch = adapters.LoraBatch(2, 16, device="cpu")
+
+    class Offsets:
+        device = "cuda:1"
+
+    batch.offsets = Offsets()
+    batch.assign(Ids())
+    assert seen == [1] and current == [0]
+    current[0] = 1
+    batch.assign(Ids())
+    assert seen == [1, 1] and current == [1]
