@@ -137,3 +137,24 @@ def test_batch_on_another_device_than_the_current_one(monkeypatch):
     current[0] = 1
     batch.assign(Ids())
     assert seen == [1, 1] and current == [1]
+
+
+def test_missing_and_misshapen_tensors_are_named():
+    z = torch.zeros
+    lg, off, cnt = z((4, 8)), z(9, dtype=torch.int32), z(9, dtype=torch.int32)
+    x, a = z((4, 16), dtype=torch.bfloat16), z((1, 2, 16), dtype=torch.bfloat16)
+    o1, tok = z(2, dtype=torch.int32), z(4, dtype=torch.int32)
+    loss = fm.moe_balance_loss
+    assert "logits is missing" in _refused(loss, None, off, z(2), cnt, z(8), z(64, dtype=torch.uint8))
+    assert "logits: expected 2 dimensions" in _refused(loss, z(8), off, z(2), cnt, z(8), z(64, dtype=torch.uint8))
+    grad = fm.moe_route_backward
+    assert "logits is missing" in _refused(grad, None, None, None, None, None, 1.0, cnt, z(2), lg)
+    assert "logits: expected 2 dimensions" in _refused(grad, z(8), None, None, None, None, 1.0, cnt, z(2), lg)
+    lora = fm.moe_lora
+    assert "x is missing" in _refused(lora, None, a, a, None, o1, tok, None, z((4, 2)), z((4, 16)))
+    assert "x: expected 2 dimensions" in _refused(lora, x[0], a, a, None, o1, tok, None, z((4, 2)), z((4, 16)))
+    assert "lora_b is missing" in _refused(lora, x, a, None, None, o1, tok, None, z((4, 2)), z((4, 16)))
+    back = fm.moe_lora_backward
+    assert "lora_b: expected 3 dimensions" in _refused(back, x, a, a[0], None, o1, tok, z((4, 2)), x, None, None, a, a, tok)
+    assert "x is missing" in _refused(back, None, a, a, None, o1, tok, z((4, 2)), x, None, None, a, a, tok)
+    assert "ws is missing" in _refused(fm._bytes, "moe_balance_loss", None, 0)
