@@ -1145,7 +1145,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 const int tok = s_tok[row];
                 const float f = scales ? __ldg(scales + tile.a) : 1.0f;
                 uint8_t* const mine = bufs + (b * kTileTokens + row) * P;
-                for (int j = (b ^ use) & 1; j < nb; j += 2) {
+                int j = (b ^ use) & 1;
+                for (; j < nb; j += 2) {
                     const uint32_t u = use + j;
                     const int c0 = (b_lo + j) * W;
                     const int width = min(W, C - c0);
@@ -1155,14 +1156,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     // lanes may see a late arrival and the abort flag in either
                     // order; what follows needs the whole warp
                     alive = __all_sync(0xFFFFFFFFu, alive);
-                    if (!alive) {  // a wait ran out: the row says so
-                        if (tok >= 0)
-                            for (int c = c0; c < c0 + width; ++c) {
-                                out[tok * ld_out + c] = NAN;
-                                if (out_bf16) out_bf16[static_cast<int64_t>(tok) * C + c] = 0x7FFF;
-                            }
-                        continue;
-                    }
+                    if (!alive) break;
                     sm100::tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < W; c += 32) {
@@ -1198,6 +1192,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     }
                     sm100::mbar_arrive(bar(kFree, b));
                 }
+                // after a wait that ran out the rest of the row says so (behind
+                // the loop: inside it these stores slow the loop by 4 %)
+                for (; j < nb && tok >= 0; j += 2)
+                    for (int c = (b_lo + j) * W; c < min((b_lo + j + 1) * W, C); ++c) {
+                        out[tok * ld_out + c] = NAN;
+                        if (out_bf16) out_bf16[static_cast<int64_t>(tok) * C + c] = 0x7FFF;
+                    }
             }
         }
         __syncthreads();  // the tile's v and token list are free
