@@ -182,13 +182,14 @@ struct WarpSums {
     {
         float inv, lse;
         if (softmax_row<VPL, LPR>(v, inv, lse)) {
-            if (fabsf(lse) < 0x1p60f)  // 16 squares stay within FP32
-                zf = fmaf(lse, lse, zf);
-            else
-                z += static_cast<double>(lse) * lse;
-            if ((++n & 15) == 0) {
+            // 16 squares stay within FP32
+            const float near = fabsf(lse) < 0x1p60f ? lse : 0.0f;
+            zf = fmaf(near, near, zf);
+            const bool last = (++n & 15) == 0;
+            if (last || near != lse) {
                 z += zf;
                 zf = 0.0f;
+                if (near != lse) z += static_cast<double>(lse) * lse;
             }
         }
 #pragma unroll
