@@ -394,8 +394,11 @@ constexpr int rows_at_once()  // rows that a lane works on side by side
     return VPL <= 8 ? 2 : 1;
 }
 
+// (One block fits an SM.  Saying so for the short rows keeps the compiler from
+// spilling to 40 registers; for the long ones it changed nothing or, at 512
+// experts, cost 2 %.)
 template <int VPL, int LPR>
-__global__ void __launch_bounds__(kLossWarps * 32)
+__global__ void __launch_bounds__(kLossWarps * 32, VPL <= 8 ? 1 : 0)
     balance_bulk_kernel(const float* __restrict__ logits, int64_t T, int E, int rows, float* __restrict__ part,
                         double* __restrict__ part_z, int* __restrict__ part_n, Waits waits)
 {
