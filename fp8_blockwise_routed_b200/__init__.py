@@ -215,13 +215,14 @@ def _bytes(what: str, t, dev: int):
     return t.data_ptr(), t.nbytes
 
 
-def _shape(what: str, name: str, t, dims: int):
-    """Sizes of the tensor that the others are checked against."""
-    if t is None:
-        _refuse(what, f"{name} is missing")
-    if t.dim() != dims:
-        _refuse(what, f"{name}: expected {dims} dimensions, got {tuple(t.shape)}")
-    return t.shape
+def _refuse_shapes(what: str, *tensors):
+    """For sizes that could not be unpacked: (name, tensor, dimensions) each."""
+    for name, t, dims in tensors:
+        if t is None:
+            _refuse(what, f"{name} is missing")
+        if t.dim() != dims:
+            _refuse(what, f"{name}: expected {dims} dimensions, got {tuple(t.shape)}")
+    raise
 
 
 def _device(what: str, name: str, t) -> int:
@@ -612,7 +613,10 @@ def moe_balance_loss(logits, expert_offsets, loss, counts, prob_mean, ws, stream
     moe_route's expert_offsets [E+1] -> loss [2] FP32 (balance, z), counts
     [E+1] int32 (pairs per expert, then the counted tokens) and prob_mean [E]."""
     what = "moe_balance_loss"
-    T, E = _shape(what, "logits", logits, 2)
+    try:
+        T, E = logits.shape
+    except (AttributeError, ValueError):
+        _refuse_shapes(what, ("logits", logits, 2))
     dev = _device(what, "logits", logits)
     f32, i32 = torch.float32, torch.int32
     _call(lib().moe_balance_loss, what, dev, stream, _arg(what, "logits", logits, f32, (T, E), dev), T, E,
@@ -628,13 +632,15 @@ def moe_route_backward(logits, topk_ids, topk_w, y, dout, routed_scaling, counts
     counts (moe_balance_loss) with d_loss [2] FP32 that of the balance and z
     losses.  Either pair may be None."""
     what = "moe_route_backward"
-    T, E = _shape(what, "logits", logits, 2)
+    try:
+        T, E = logits.shape
+        _, k, H = (0, 0, 0) if y is None else y.shape
+    except (AttributeError, ValueError):
+        _refuse_shapes(what, ("logits", logits, 2), ("y", y, 3))
     dev = _device(what, "logits", logits)
     f32, i32 = torch.float32, torch.int32
-    k = H = 0
     p_ids = p_w = p_y = p_dout = p_counts = p_loss = None
     if y is not None:
-        _, k, H = _shape(what, "y", y, 3)
         p_ids = _arg(what, "topk_ids", topk_ids, i32, (T, k), dev)
         p_w = _arg(what, "topk_w", topk_w, f32, (T, k), dev)
         p_y = _arg(what, "y", y, f32, (T, k, H), dev)
@@ -661,8 +667,11 @@ def moe_lora(x, lora_a, lora_b, scales, adapter_offsets, sorted_tokens, base, v,
     FP32 (kept for the backward call); out [T, N] FP32; out_bf16 [T, N] or
     None.  x, base and out may have strided rows."""
     what = "moe_lora"
-    T, K = _shape(what, "x", x, 2)
-    n, R, N = _shape(what, "lora_b", lora_b, 3)
+    try:
+        T, K = x.shape
+        n, R, N = lora_b.shape
+    except (AttributeError, ValueError):
+        _refuse_shapes(what, ("x", x, 2), ("lora_b", lora_b, 3))
     dev = _device(what, "x", x)
     f32, i32, b16 = torch.float32, torch.int32, torch.bfloat16
     p_x, ld_x = _rows(what, "x", x, b16, T, K, dev)
@@ -687,8 +696,11 @@ def moe_lora_backward(x, lora_a, lora_b, scales, adapter_offsets, sorted_tokens,
     plus the adapters' part, for tokens with an adapter; None: not wanted),
     d_a [n, rank, K] and d_b [n, rank, N] FP32.  v as moe_lora wrote it."""
     what = "moe_lora_backward"
-    T, K = _shape(what, "x", x, 2)
-    n, R, N = _shape(what, "lora_b", lora_b, 3)
+    try:
+        T, K = x.shape
+        n, R, N = lora_b.shape
+    except (AttributeError, ValueError):
+        _refuse_shapes(what, ("x", x, 2), ("lora_b", lora_b, 3))
     dev = _device(what, "x", x)
     f32, i32, b16 = torch.float32, torch.int32, torch.bfloat16
     p_x, ld_x = _rows(what, "x", x, b16, T, K, dev)

@@ -130,7 +130,7 @@ const char* moe_status_string(int status)
     }
 }
 
-int moe_abi_version(void) { return (1 << 16) | 1; }
+int moe_abi_version(void) { return (1 << 16) | 2; }
 
 const char* moe_last_error(void) { return g_last_error; }
 

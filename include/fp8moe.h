@@ -568,7 +568,13 @@ MOE_API int moe_route_backward(const float* logits, int64_t T, int E, const int3
  * of 4.  No workspace, no device status; v and out overlap nothing that is
  * read (but base).  One to two launches, two or three with the backward call;
  * a wait inside a kernel that expires leaves NaN in the rows concerned.  An
- * element of v or dv within 2^-9 of FP32's largest counts as infinite.
+ * element of v or dv within 2^-9 of FP32's largest counts as infinite.  v and
+ * dv enter their products as three BF16 terms: where a finite one meets an
+ * infinite entry of lora_a, lora_b, x or dout, the sum may be NaN where the
+ * formula gives infinity.  The kernel is chosen by T, K, N, rank and
+ * n_adapters: a few adapters in use of many resident ones are slower than
+ * the same few passed alone, and moe_lora_backward writes the gradients of
+ * all of them.
  *
  * moe_lora_backward -- its gradients, for dout the gradient of out:
  *   dv[p, r]     = scales[a] * sum_c dout[t, c] lora_b[a, r, c]
