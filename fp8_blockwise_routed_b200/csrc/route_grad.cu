@@ -711,7 +711,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 }
                 acc[0] += __shfl_xor_sync(0xFFFFFFFFu, acc[0], 2);
                 acc[0] += __shfl_xor_sync(0xFFFFFFFFu, acc[0], 1);
-                // NaN once a wait ran out: columns, or the tail's leave to write, are missing
+                // NaN once a wait ran out: columns, or the tail's leave to write, are
+                // missing.  (The warp arrives below all the same, also out of turn, but
+                // never before its NaN is in every token that the arrival can complete.)
                 if ((lane & 3) == 0) s_red[buf][warp][j0 + lane / 4] = ok ? acc[0] : NAN;
             }
             __syncwarp();
@@ -768,8 +770,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             const float wj = id >= 0 ? __ldg(w + t * k + lane) : 0.0f;
             const int buf = static_cast<int>(n % kDotBufs);
             ok = ok && wait(&s_dots[buf], static_cast<int>(n / kDotBufs));
-            // a dot warp that gave up arrives all the same, behind the flag
-            ok = __all_sync(0xFFFFFFFFu, ok && !*static_cast<volatile int*>(&s_abort));
             float s = 0.0f;
             if (id >= 0) {
 #pragma unroll
