@@ -1672,7 +1672,9 @@ cudaError_t launch_lora(const LoraRows& rows, int R, const LoraProduct& p, bool*
     // 2048 to 2048, 11 / 15 us; 400 on 4, 5120 to 1536, 14 / 16.5; 512 on one,
     // 5120 to 5120, 23 / 19.5, of rank 32 on six 16 / 18; 4096 on 256 of rank 16,
     // 2048 to 2048, 31.5 / 41.5; 2048 on 200 of rank 64, 5120 to 5120, 128 / 113
-    // (two tiles of 8 tokens each read an adapter's ranks).
+    // (two tiles of 8 tokens each read an adapter's ranks).  All with the adapters
+    // in use: n counts the resident ones, the host does not know the others
+    // (8000 tokens on 4 of 1024 of rank 64 take 256 us here, 101 with n = 4).
     if (rows.T <= (R <= 32 ? 512 : 384) || rows.T < (R <= 32 ? 24 : 8) * static_cast<int64_t>(rows.n)) {
         const SmallArgs a{p.x,    p.ldx, p.C1,   p.w1,      p.f1,  p.v,      t,         p.u, ut, p.w2,
                           p.C2, p.f2,  p.base, p.ld_base, p.out, p.ld_out, p.out_bf16};

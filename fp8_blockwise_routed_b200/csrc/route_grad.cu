@@ -617,7 +617,7 @@ __device__ __forceinline__ void grad_row(float (&v)[VPL], bool losses, const flo
 // across tokens), eight warps take the dots out of shared memory, and four
 // more finish the tokens (sum of the warps' dots, softmax gradient, the row's
 // write), so that no load waits for a token's end.  (One block per token with
-// direct loads: 137 us against 112 at T = 4096, H = 5120, k = 8.)
+// direct loads: 137 us against 113 at T = 4096, H = 5120, k = 8.)
 constexpr int kDotWarps = 8;
 constexpr int kTailWarps = 4;
 constexpr int kGradThreads = (kDotWarps + 1 + kTailWarps) * 32;
